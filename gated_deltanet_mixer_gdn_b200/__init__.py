@@ -14,6 +14,7 @@ There is no CPU path: if the library is missing the calls raise.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
 import threading
 from typing import Dict, Optional, Sequence
@@ -32,6 +33,8 @@ EXPORTS = ("gdn_prefill_workspace_size", "gdn_prefill", "gdn_prefill_out_workspa
            "gdn_in_proj", "gdn_out_proj", "gdn_prefill_hidden_workspace_size", "gdn_prefill_hidden",
            "gdn_prefill_hidden_varlen_workspace_size", "gdn_prefill_hidden_varlen",
            "gdn_prefill_noalloc", "gdn_last_device_error", "gdn_set_decode_wait_limit", "gdn_test_decode_stop_copies_at",
+           "gdn_quant_scale_bytes", "gdn_quantize", "gdn_dequantize", "gdn_proj_quant_workspace_size",
+           "gdn_in_proj_quant", "gdn_out_proj_quant", "gdn_copy_slots", "gdn_compact_slots",
            "gdn_status_string",
            "gdn_version")
 
@@ -105,6 +108,22 @@ def load_library() -> ctypes.CDLL:
         L.gdn_prefill_varlen_slots.restype = ctypes.c_int
         L.gdn_prefill_varlen_slots.argtypes = [dp, wp, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                                vp, sz, vp]
+        L.gdn_quant_scale_bytes.restype = sz
+        L.gdn_quant_scale_bytes.argtypes = [i32, i32, i32]
+        L.gdn_quantize.restype = ctypes.c_int
+        L.gdn_quantize.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp]
+        L.gdn_dequantize.restype = ctypes.c_int
+        L.gdn_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp]
+        L.gdn_proj_quant_workspace_size.restype = sz
+        L.gdn_proj_quant_workspace_size.argtypes = [i32, i32, i32]
+        L.gdn_in_proj_quant.restype = ctypes.c_int
+        L.gdn_in_proj_quant.argtypes = [dp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.gdn_out_proj_quant.restype = ctypes.c_int
+        L.gdn_out_proj_quant.argtypes = [dp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.gdn_copy_slots.restype = ctypes.c_int
+        L.gdn_copy_slots.argtypes = [dp, i32, vp, vp, i32, vp, vp, vp]
+        L.gdn_compact_slots.restype = ctypes.c_int
+        L.gdn_compact_slots.argtypes = [dp, i32, vp, i32, vp, vp, vp, vp]
         L.gdn_last_device_error.restype = ctypes.c_int
         L.gdn_last_device_error.argtypes = []
         L.gdn_set_decode_wait_limit.restype = ctypes.c_int
@@ -453,6 +472,141 @@ def out_proj(y, w_out, *, dims: Dims = MODEL, out=None):
     return out
 
 
+QUANT_FORMATS = {"nvfp4": 0, "mxfp4": 1}
+
+
+@dataclasses.dataclass(frozen=True)
+class QuantTensor:
+    """Rows held in microscaled 4 bits (layouts in ``include/gdn.h``): what ``quantize`` returns and
+    the 4-bit projections take as weights.  codes uint8 [rows, K/2]; scales uint8 [row blocks of 128,
+    tiles, 512]; row_scale f32 [rows]."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    row_scale: torch.Tensor
+    format: str
+
+    @property
+    def shape(self):
+        return int(self.codes.shape[0]), 2 * int(self.codes.shape[1])
+
+
+def _quant_format(format: str) -> int:
+    if format not in QUANT_FORMATS:
+        raise ValueError(f"format must be one of {sorted(QUANT_FORMATS)}, got {format!r}")
+    return QUANT_FORMATS[format]
+
+
+def _quant_checked(q: QuantTensor, name: str, device: torch.device):
+    if not isinstance(q, QuantTensor):
+        raise TypeError(f"{name} must be a QuantTensor")
+    rows, K = q.shape
+    _need(q.codes, torch.uint8, f"{name}.codes", device)
+    _need(q.scales, torch.uint8, f"{name}.scales", device)
+    _need(q.row_scale, torch.float32, f"{name}.row_scale", device)
+    if q.codes.dim() != 2 or q.row_scale.numel() != rows or \
+            q.scales.numel() != load_library().gdn_quant_scale_bytes(_quant_format(q.format), rows, K):
+        raise ValueError(f"{name}: codes, scales and row_scale do not belong together")
+    return _quant_format(q.format), rows, K
+
+
+def quantize(x, format: str = "nvfp4", *, out: Optional[QuantTensor] = None) -> QuantTensor:
+    """x bf16 [rows, K] (K a multiple of 64) as microscaled 4-bit rows: "nvfp4" (blocks of 16 with E4M3
+    scales and a power of two per row) or "mxfp4" (blocks of 32 with power-of-two scales)."""
+    dev = _device_of(x)
+    fmt = _quant_format(format)
+    L = load_library()
+    _need(x, torch.bfloat16, "x", dev)
+    if x.dim() != 2:
+        raise ValueError("quantize: x must be [rows, K]")
+    rows, K = int(x.shape[0]), int(x.shape[1])
+    if K == 0 or K % 64:
+        raise ValueError("quantize: K must be a multiple of 64")
+    if out is None:
+        tile_blocks = L.gdn_quant_scale_bytes(fmt, 128, K) // 512
+        out = QuantTensor(torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+                          torch.empty(((rows + 127) // 128, tile_blocks, 512), dtype=torch.uint8, device=dev),
+                          torch.empty((rows,), dtype=torch.float32, device=dev), format)
+    elif _quant_checked(out, "out", dev) != (fmt, rows, K):
+        raise ValueError("quantize: out has another format or shape")
+    with torch.cuda.device(dev):
+        st = L.gdn_quantize(fmt, rows, K, _ptr(x), _ptr(out.codes), _ptr(out.scales), _ptr(out.row_scale), _stream(dev))
+    _check(st, "gdn_quantize")
+    return out
+
+
+def dequantize(q: QuantTensor, *, out=None):
+    """The values that 4-bit rows stand for, bf16 [rows, K] (exact)."""
+    dev = _device_of(q.codes)
+    fmt, rows, K = _quant_checked(q, "q", dev)
+    if out is None:
+        out = torch.empty((rows, K), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, torch.bfloat16, "out", dev)
+        if tuple(out.shape) != (rows, K):
+            raise ValueError("dequantize: out shape")
+    with torch.cuda.device(dev):
+        st = load_library().gdn_dequantize(fmt, rows, K, _ptr(q.codes), _ptr(q.scales), _ptr(q.row_scale), _ptr(out),
+                                           _stream(dev))
+    _check(st, "gdn_dequantize")
+    return out
+
+
+def _proj_out(out, widths, T: int, dev: torch.device, what: str):
+    if out is None:
+        return [torch.empty((T, w), dtype=torch.bfloat16, device=dev) for w in widths]
+    for t, w in zip(out, widths):
+        _need(t, torch.bfloat16, f"{what} out", dev)
+        if tuple(t.shape) != (T, w):
+            raise ValueError(f"{what}: out shape")
+    return list(out)
+
+
+def in_proj_quant(x, w_in: QuantTensor, *, dims: Dims = MODEL, out=None):
+    """in_proj on 4-bit operands: x bf16 [T, hidden] is quantised token by token in the weights'
+    format, w_in holds the stacked weights [C + Vh*D + 2*Vh, hidden] (qkv, z, b, a rows) quantised.
+    Returns (qkv [T,C], z [T,Vh*D], a [T,Vh], b [T,Vh]) bf16."""
+    dev = _device_of(x)
+    _need(x, torch.bfloat16, "x", dev)
+    fmt, N, K = _quant_checked(w_in, "w_in", dev)
+    C, VD, Vh = dims.conv_channels, dims.value_width, dims.num_v_heads
+    if x.dim() != 2 or int(x.shape[1]) != K or N != C + VD + 2 * Vh:
+        raise ValueError("in_proj_quant: shape mismatch")
+    T = int(x.shape[0])
+    L = load_library()
+    qkv, z, a, b = _proj_out(out, (C, VD, Vh, Vh), T, dev, "in_proj_quant")
+    ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
+    ws = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+    dc = _dims_c(dims)
+    with torch.cuda.device(dev):
+        st = L.gdn_in_proj_quant(ctypes.byref(dc), fmt, T, K, _ptr(x), _ptr(w_in.codes), _ptr(w_in.scales),
+                                 _ptr(w_in.row_scale), _ptr(qkv), _ptr(z), _ptr(b), _ptr(a), _ptr(ws), ws_bytes,
+                                 _stream(dev))
+    _check(st, "gdn_in_proj_quant")
+    return qkv, z, a, b
+
+
+def out_proj_quant(y, w_out: QuantTensor, *, dims: Dims = MODEL, out=None):
+    """out_proj on 4-bit operands: y bf16 [T, Vh*D], w_out [hidden, Vh*D] quantised.  Returns out bf16
+    [T, hidden]."""
+    dev = _device_of(y)
+    _need(y, torch.bfloat16, "y", dev)
+    fmt, hidden, K = _quant_checked(w_out, "w_out", dev)
+    if y.dim() != 2 or K != dims.value_width or int(y.shape[1]) != K:
+        raise ValueError("out_proj_quant: shape mismatch")
+    T = int(y.shape[0])
+    L = load_library()
+    out, = _proj_out(None if out is None else [out], (hidden,), T, dev, "out_proj_quant")
+    ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
+    ws = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+    dc = _dims_c(dims)
+    with torch.cuda.device(dev):
+        st = L.gdn_out_proj_quant(ctypes.byref(dc), fmt, T, hidden, _ptr(y), _ptr(w_out.codes), _ptr(w_out.scales),
+                                  _ptr(w_out.row_scale), _ptr(out), _ptr(ws), ws_bytes, _stream(dev))
+    _check(st, "gdn_out_proj_quant")
+    return out
+
+
 def _slot_tables(slots, n, dev):
     if isinstance(slots, torch.Tensor):
         host = slots.detach().to("cpu", torch.int32).contiguous()
@@ -518,6 +672,68 @@ def prefill_varlen_slots(cu_seqlens, slots, qkv, z, a, b, weights, state_pool, c
     return out
 
 
+def _pool_checked(state_pool, conv_pool, dims: Dims, what: str):
+    dev = _device_of(state_pool)
+    _need(state_pool, torch.float32, "state_pool", dev)
+    _need(conv_pool, torch.float32, "conv_pool", dev)
+    P = int(state_pool.shape[0])
+    if tuple(state_pool.shape) != (P, dims.num_v_heads, dims.head_dim, dims.head_dim) or \
+            tuple(conv_pool.shape) != (P, dims.conv_width - 1, dims.conv_channels):
+        raise ValueError(f"{what}: pool shapes")
+    return dev, P
+
+
+def _host_table(rows) -> torch.Tensor:
+    t = rows.detach() if isinstance(rows, torch.Tensor) else torch.tensor(list(rows), dtype=torch.int64)
+    if t.dim() != 1 or t.dtype not in (torch.int32, torch.int64):
+        raise TypeError("pool rows must be a list or a one-dimensional int32 / int64 tensor")
+    t = t.to("cpu", torch.int64)
+    if t.numel() and (int(t.min()) < -(1 << 31) or int(t.max()) >= 1 << 31):
+        raise ValueError("pool rows out of range")
+    return t.to(torch.int32).contiguous()
+
+
+def copy_slots(src, dst, state_pool, conv_pool, *, dims: Dims = MODEL):
+    """Pool row dst[i] becomes what row src[i] held before the call (zero where src[i] is -1), for all
+    pairs at once and in place: forks (one source, several destinations), reorderings, swaps and
+    cycles.  src, dst: lists or int32 / int64 tensors (host ones do not synchronise), no dst twice."""
+    dev, P = _pool_checked(state_pool, conv_pool, dims, "copy_slots")
+    s, d = _host_table(src), _host_table(dst)
+    if s.numel() != d.numel():
+        raise ValueError("copy_slots: one source per destination")
+    dc = _dims_c(dims)
+    with torch.cuda.device(dev):
+        st = load_library().gdn_copy_slots(ctypes.byref(dc), int(d.numel()), ctypes.c_void_p(s.data_ptr()),
+                                           ctypes.c_void_p(d.data_ptr()), P, _ptr(state_pool), _ptr(conv_pool),
+                                           _stream(dev))
+    _check(st, "gdn_copy_slots")
+
+
+def free_slots(slots, state_pool, conv_pool, *, dims: Dims = MODEL):
+    """Clears pool rows (zero state and history: a new sequence starts from them)."""
+    d = _host_table(slots)
+    copy_slots(torch.full_like(d, -1), d, state_pool, conv_pool, dims=dims)
+
+
+def compact_slots(live, state_pool, conv_pool, *, clear: bool = False, dims: Dims = MODEL):
+    """Moves the live pool rows (live: one truth value per row) to the front of the pool: those before
+    the live count stay, those behind it fill the free rows before it in ascending order.  ``clear``
+    zeroes the rows behind.  Returns the new row of each old row, int32 on the host, -1 where not live."""
+    dev, P = _pool_checked(state_pool, conv_pool, dims, "compact_slots")
+    flags = live.detach().to("cpu") if isinstance(live, torch.Tensor) else torch.tensor(list(live))
+    flags = (flags != 0).to(torch.uint8).contiguous()
+    if tuple(flags.shape) != (P,):
+        raise ValueError("compact_slots: one flag per pool row")
+    remap = torch.empty((P,), dtype=torch.int32)
+    dc = _dims_c(dims)
+    with torch.cuda.device(dev):
+        st = load_library().gdn_compact_slots(ctypes.byref(dc), P, ctypes.c_void_p(flags.data_ptr()), int(bool(clear)),
+                                              _ptr(state_pool), _ptr(conv_pool), ctypes.c_void_p(remap.data_ptr()),
+                                              _stream(dev))
+    _check(st, "gdn_compact_slots")
+    return remap
+
+
 def last_device_error() -> int:
     """The device error word (0, or the code of the first bounded wait that ran out); cleared by reading."""
     return load_library().gdn_last_device_error()
@@ -535,5 +751,7 @@ def weights_to(weights: Dict[str, torch.Tensor], device) -> Dict[str, torch.Tens
     return {k: v.to(device).contiguous() for k, v in weights.items()}
 
 
-__all__ = ["prefill", "prefill_out", "prefill_schedule", "prefill_varlen", "decode", "decode_multi", "decode_slots", "in_proj", "out_proj", "prefill_hidden", "prefill_hidden_varlen", "prefill_varlen_slots", "last_device_error", "set_decode_wait_limit", "status_string", "load_library",
+__all__ = ["prefill", "prefill_out", "prefill_schedule", "prefill_varlen", "decode", "decode_multi", "decode_slots", "in_proj", "out_proj", "prefill_hidden", "prefill_hidden_varlen", "prefill_varlen_slots",
+           "QuantTensor", "QUANT_FORMATS", "quantize", "dequantize", "in_proj_quant", "out_proj_quant", "copy_slots",
+           "free_slots", "compact_slots", "last_device_error", "set_decode_wait_limit", "status_string", "load_library",
            "GdnError", "Dims", "MODEL", "LIB_PATH", "EXPORTS", "weights_to"]

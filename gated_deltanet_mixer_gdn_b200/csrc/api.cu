@@ -6,10 +6,13 @@
 #include <cudaTypedefs.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <utility>
 #include <vector>
 
 #include "../../include/gdn.h"
@@ -19,7 +22,10 @@
 #include "decode.cuh"
 #include "gemm.cuh"
 #include "inproj.cuh"
+#include "pool.cuh"
 #include "prep.cuh"
+#include "qproj.cuh"
+#include "quant.cuh"
 
 namespace {
 
@@ -1255,10 +1261,361 @@ const char* gdn_status_string(int status) {
         case GDN_ERR_CUDA: return "CUDA error";
         case GDN_ERR_WORKSPACE: return "workspace missing or too small";
         case GDN_ERR_TIMEOUT: return "bounded device wait expired";
+        case GDN_ERR_HOST_MEMORY: return "out of host memory";
         default: return "unknown status";
     }
 }
 
 int gdn_version(void) { return 100; }
+
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------- 4-bit operands
+int check_format(int32_t format) {
+    return format == GDN_NVFP4 || format == GDN_MXFP4 ? GDN_OK : GDN_ERR_INVALID_ARG;
+}
+
+// Contraction widths the 4-bit operands support: whole products of 64 elements.
+bool quant_width_ok(int32_t K) { return K > 0 && K % qproj::kMmaK == 0; }
+
+size_t quant_scale_bytes(int format, int64_t rows, int K) {
+    return (size_t)((rows + 127) / 128) * quant::scale_tiles(format, K) * quant::kTileBytes;
+}
+
+int quantize_launch(int format, int32_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
+                    float* row_scale, cudaStream_t stream) {
+    quant::Params p{x, codes, scales, row_scale, rows, K, quant::scale_tiles(format, K)};
+    // threads per row: one unit of 16 elements each, up to 512 (then two or more); at least 256 per CTA
+    const int units = K / quant::kUnit;
+    const int gx = units >= quant::kMaxGroup ? quant::kMaxGroup : (units + 31) / 32 * 32;
+    const int gy = gx >= 256 ? 1 : 256 / gx;
+    const dim3 block(gx, gy), grid((rows + gy - 1) / gy);
+    if (format == GDN_NVFP4) gdn_quantize_kernel<quant::kNvfp4><<<grid, block, 0, stream>>>(p);
+    else gdn_quantize_kernel<quant::kMxfp4><<<grid, block, 0, stream>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
+// 2-D map over packed 4-bit codes [rows][K / 2 bytes], box of 128 bytes (256 elements) x box_rows.
+bool make_code_map(CUtensorMap* m, const uint8_t* base, int32_t K, int64_t rows, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int BN>
+int qproj_tiles(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
+    CUtensorMap mW, mX;
+    if (!make_code_map(&mW, cw, p.K, p.N, qproj::BM) || !make_code_map(&mX, cx, p.K, p.T, BN)) return GDN_ERR_CUDA;
+    using C = qproj::Cfg<BN>;
+    auto kernel = gdn_qproj_kernel<FMT, BN>;
+    int st = smem_optin(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES);
+    if (st != GDN_OK) return st;
+    const dim3 grid((p.N + qproj::BM - 1) / qproj::BM, (p.T + BN - 1) / BN);
+    kernel<<<grid, qproj::kThreads, C::SMEM_BYTES, stream>>>(mW, mX, p);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int FMT>
+int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
+    if (p.T <= 16) return qproj_tiles<FMT, 16>(cx, cw, p, stream);
+    if (p.T <= 64) return qproj_tiles<FMT, 64>(cx, cw, p, stream);
+    return qproj_tiles<FMT, 128>(cx, cw, p, stream);
+}
+
+// Workspace of a 4-bit projection: the quantised tokens.
+struct QuantRows {
+    size_t off_scales, off_row_scale, bytes;
+};
+QuantRows quant_rows(int format, int64_t T, int K) {
+    QuantRows q{};
+    q.off_scales = align_up((size_t)T * (K / 2));
+    q.off_row_scale = q.off_scales + align_up(quant_scale_bytes(format, T, K));
+    q.bytes = q.off_row_scale + align_up((size_t)T * 4);
+    return q;
+}
+
+// y = x W^T on 4-bit operands: x [T][K] quantised into the workspace, then the product.
+int proj_quant(int format, int32_t T, int32_t K, int32_t N, const uint16_t* x, const uint8_t* w_codes,
+               const uint8_t* w_scales, const float* w_row_scale, const GemmSegment* seg, int nseg, void* workspace,
+               size_t workspace_bytes, void* stream) {
+    if (!x || !w_codes || !w_scales || !w_row_scale || !aligned16(x) || !aligned16(w_codes) || !aligned16(w_scales) ||
+        (reinterpret_cast<uintptr_t>(w_row_scale) & 3u))
+        return GDN_ERR_INVALID_ARG;
+    for (int i = 0; i < nseg; ++i)
+        if (seg[i].dst == nullptr || !aligned16(seg[i].dst)) return GDN_ERR_INVALID_ARG;
+    const QuantRows q = quant_rows(format, T, K);
+    if (workspace == nullptr || workspace_bytes < q.bytes) return GDN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+    int st = check_device();
+    if (st != GDN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* wsb = static_cast<uint8_t*>(workspace);
+    qproj::Params p{};
+    p.T = T;
+    p.N = N;
+    p.K = K;
+    p.tiles = quant::scale_tiles(format, K);
+    p.sx = wsb + q.off_scales;
+    p.sw = w_scales;
+    p.gx = reinterpret_cast<const float*>(wsb + q.off_row_scale);
+    p.gw = w_row_scale;
+    p.nseg = nseg;
+    for (int i = 0; i < nseg; ++i) p.seg[i] = seg[i];
+    if ((st = quantize_launch(format, T, K, x, wsb, wsb + q.off_scales,
+                              reinterpret_cast<float*>(wsb + q.off_row_scale), s)) != GDN_OK)
+        return st;
+    return format == GDN_NVFP4 ? qproj_launch<quant::kNvfp4>(wsb, w_codes, p, s)
+                                    : qproj_launch<quant::kMxfp4>(wsb, w_codes, p, s);
+}
+
+// ---------------------------------------------------------------- pool rows
+// Pairs (src[i], dst[i]) of pool rows, src -1 = clear, all reads before all writes.  Checked by the caller.
+struct RowPair {
+    int32_t src, dst;
+};
+
+int pool_flush(pool::Params& p, int nsm, cudaStream_t stream) {
+    if (p.nset == 0) return GDN_OK;
+    int st = smem_optin(reinterpret_cast<const void*>(gdn_pool_kernel), pool::SMEM_BYTES);
+    if (st != GDN_OK) return st;
+    gdn_pool_kernel<<<p.ntask < nsm ? p.ntask : nsm, 32, pool::SMEM_BYTES, stream>>>(p);
+    p.nset = p.ntask = 0;
+    return cuda_status(cudaGetLastError());
+}
+
+// Groups the pairs into sets linked by a shared row and launches them, at most pool::kMaxOps
+// destinations a launch.  Sets share no rows, so launches do not depend on one another.
+int pool_launch(const gdn_dims* dims, std::vector<RowPair> pairs, int32_t pool_rows, float* state, float* conv,
+                cudaStream_t stream) {
+    // a row kept in place is neither read nor written
+    size_t n = 0;
+    for (const RowPair& r : pairs)
+        if (r.src != r.dst) pairs[n++] = r;
+    pairs.resize(n);
+    if (n == 0) return GDN_OK;
+    int dev = 0, nsm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    std::vector<int32_t> root((size_t)pool_rows);
+    for (int32_t i = 0; i < pool_rows; ++i) root[i] = i;
+    auto find = [&](int32_t i) {
+        while (root[i] != i) i = root[i] = root[root[i]];
+        return i;
+    };
+    std::vector<unsigned char> is_dst((size_t)pool_rows, 0);
+    for (const RowPair& r : pairs) {
+        if (r.src >= 0) root[find(r.src)] = find(r.dst);
+        is_dst[r.dst] = 1;
+    }
+    // pairs of a set next to each other, a set's pairs by source
+    std::vector<std::pair<int64_t, int32_t>> key(n);
+    for (size_t i = 0; i < n; ++i) key[i] = {((int64_t)find(pairs[i].dst) << 32) | (uint32_t)(pairs[i].src + 1), (int32_t)i};
+    std::sort(key.begin(), key.end());
+    auto set_end = [&](size_t i) {
+        size_t j = i;
+        while (j < n && (key[j].first >> 32) == (key[i].first >> 32)) ++j;
+        return j;
+    };
+    // a set that overwrites one of its sources is moved by one launch
+    auto overwrites = [&](size_t i, size_t j) {
+        for (size_t k = i; k < j; ++k) {
+            const int32_t src = pairs[key[k].second].src;
+            if (src >= 0 && is_dst[src]) return true;
+        }
+        return false;
+    };
+    for (size_t i = 0; i < n; i = set_end(i))
+        if (set_end(i) - i > (size_t)pool::kMaxOps && overwrites(i, set_end(i))) return GDN_ERR_UNSUPPORTED;
+
+    pool::Params p{};
+    p.base[0] = reinterpret_cast<uint8_t*>(state);
+    p.base[1] = reinterpret_cast<uint8_t*>(conv);
+    p.row_bytes[0] = (uint32_t)dims->num_v_heads * 128 * 128 * 4;
+    p.row_bytes[1] = 3u * (2 * dims->num_k_heads + dims->num_v_heads) * 128 * 4;
+    p.pool_rows = pool_rows;
+    // a row's bytes per task: whole stages when the rows fill the device several times over, else
+    // smaller ranges so that every SM has some
+    const uint64_t total = (uint64_t)n * (p.row_bytes[0] + p.row_bytes[1]);
+    const uint32_t stage = total >= (uint64_t)nsm * pool::kStages * pool::kStageBytes ? pool::kStageBytes : 8192;
+    int nsrc = 0, nop = 0;
+    for (size_t i = 0; i < n;) {
+        size_t j = set_end(i);
+        if (j - i > (size_t)pool::kMaxOps) j = i + pool::kMaxOps;  // (one source, or clears: any part of it)
+        if (nop + (int)(j - i) > pool::kMaxOps) {
+            const int st = pool_flush(p, nsm, stream);
+            if (st != GDN_OK) return st;
+            nsrc = nop = 0;
+        }
+        pool::Set& e = p.set[p.nset++];
+        e.task0 = p.ntask;
+        e.src0 = (uint16_t)nsrc;
+        e.op0 = (uint16_t)nop;
+        for (size_t k = i; k < j; ++k) {
+            const RowPair& r = pairs[key[k].second];
+            if (r.src >= 0 && (nsrc == e.src0 || p.src[nsrc - 1] != r.src)) p.src[nsrc++] = r.src;
+            p.op[nop++] = pool::Op{r.dst, r.src >= 0 ? nsrc - 1 - e.src0 : pool::kZero};
+        }
+        e.nsrc = (uint16_t)(nsrc - e.src0);
+        e.nop = (uint16_t)(nop - e.op0);
+        uint32_t chunk = stage / (e.nsrc > 1 ? e.nsrc : 1);
+        if (chunk < 256) chunk = pool::kStageBytes / e.nsrc;  // (many sources: the whole stage)
+        e.chunk = chunk >= 128 ? chunk & ~127u : chunk & ~15u;
+        for (int k = 0; k < 2; ++k) p.ntask += (int32_t)((p.row_bytes[k] + e.chunk - 1) / e.chunk);
+        i = j;
+    }
+    return pool_flush(p, nsm, stream);
+}
+
+int check_pool(const gdn_dims* dims, int32_t pool_rows, const float* state, const float* conv) {
+    const int st = check_dims(dims);
+    if (st != GDN_OK) return st;
+    if (pool_rows < 0) return GDN_ERR_INVALID_ARG;
+    if (pool_rows > 0 && (!state || !conv || !aligned16(state) || !aligned16(conv))) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_quant_scale_bytes(int32_t format, int32_t rows, int32_t K) {
+    if (check_format(format) != GDN_OK || rows < 0 || !quant_width_ok(K)) return 0;
+    return quant_scale_bytes(format, rows, K);
+}
+
+int gdn_quantize(int32_t format, int32_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
+                 float* row_scale, void* stream) {
+    NvtxRange nvtx_range("gdn_quantize");
+    int st = check_format(format);
+    if (st != GDN_OK) return st;
+    if (rows < 0 || K <= 0) return GDN_ERR_INVALID_ARG;
+    if (!quant_width_ok(K)) return GDN_ERR_UNSUPPORTED;
+    if (rows == 0) return GDN_OK;
+    if (!x || !codes || !scales || !row_scale || !aligned16(x) || !aligned16(codes) || !aligned16(scales) ||
+        (reinterpret_cast<uintptr_t>(row_scale) & 3u))
+        return GDN_ERR_INVALID_ARG;
+    if ((st = check_device()) != GDN_OK) return st;
+    return quantize_launch(format, rows, K, x, codes, scales, row_scale, static_cast<cudaStream_t>(stream));
+}
+
+int gdn_dequantize(int32_t format, int32_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales,
+                   const float* row_scale, uint16_t* out, void* stream) {
+    NvtxRange nvtx_range("gdn_dequantize");
+    int st = check_format(format);
+    if (st != GDN_OK) return st;
+    if (rows < 0 || K <= 0) return GDN_ERR_INVALID_ARG;
+    if (!quant_width_ok(K)) return GDN_ERR_UNSUPPORTED;
+    if (rows == 0) return GDN_OK;
+    if (!out || !codes || !scales || !row_scale || !aligned16(out) || !aligned16(codes) || !aligned16(scales) ||
+        (reinterpret_cast<uintptr_t>(row_scale) & 3u))
+        return GDN_ERR_INVALID_ARG;
+    if ((st = check_device()) != GDN_OK) return st;
+    const int tiles = quant::scale_tiles(format, K);
+    const int64_t units = (int64_t)rows * (K / quant::kUnit);
+    const int64_t blocks = (units + 255) / 256;
+    const int grid = (int)(blocks < 65536 ? blocks : 65536);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (format == GDN_NVFP4)
+        gdn_dequantize_kernel<quant::kNvfp4><<<grid, 256, 0, s>>>(codes, scales, row_scale, rows, K, tiles, out);
+    else
+        gdn_dequantize_kernel<quant::kMxfp4><<<grid, 256, 0, s>>>(codes, scales, row_scale, rows, K, tiles, out);
+    return cuda_status(cudaGetLastError());
+}
+
+size_t gdn_proj_quant_workspace_size(int32_t format, int32_t T, int32_t K) {
+    if (check_format(format) != GDN_OK || T < 0 || !quant_width_ok(K)) return 0;
+    return quant_rows(format, T, K).bytes;
+}
+
+int gdn_in_proj_quant(const gdn_dims* dims, int32_t format, int32_t T, int32_t hidden, const uint16_t* x,
+                      const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scale, uint16_t* qkv,
+                      uint16_t* z, uint16_t* b, uint16_t* a, void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("gdn_in_proj_quant");
+    int st = check_dims(dims);
+    if (st != GDN_OK || (st = check_format(format)) != GDN_OK) return st;
+    if (T < 0 || hidden <= 0) return GDN_ERR_INVALID_ARG;
+    if (!quant_width_ok(hidden)) return GDN_ERR_UNSUPPORTED;
+    if (T == 0) return GDN_OK;
+    const int Vh = dims->num_v_heads, D = dims->head_dim;
+    const int C = (2 * dims->num_k_heads + Vh) * D;
+    const GemmSegment seg[4] = {GemmSegment{0, C, qkv}, GemmSegment{C, Vh * D, z}, GemmSegment{C + Vh * D, Vh, b},
+                                GemmSegment{C + Vh * D + Vh, Vh, a}};
+    return proj_quant(format, T, hidden, C + Vh * D + 2 * Vh, x, w_codes, w_scales, w_row_scale, seg, 4, workspace,
+                      workspace_bytes, stream);
+}
+
+int gdn_out_proj_quant(const gdn_dims* dims, int32_t format, int32_t T, int32_t hidden, const uint16_t* y,
+                       const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scale, uint16_t* out,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("gdn_out_proj_quant");
+    int st = check_dims(dims);
+    if (st != GDN_OK || (st = check_format(format)) != GDN_OK) return st;
+    if (T < 0 || hidden <= 0) return GDN_ERR_INVALID_ARG;
+    if (T == 0) return GDN_OK;
+    const GemmSegment seg[1] = {GemmSegment{0, hidden, out}};
+    return proj_quant(format, T, dims->num_v_heads * dims->head_dim, hidden, y, w_codes, w_scales, w_row_scale, seg, 1,
+                      workspace, workspace_bytes, stream);
+}
+
+int gdn_copy_slots(const gdn_dims* dims, int32_t n, const int32_t* src_host, const int32_t* dst_host, int32_t pool_rows,
+                   float* state_pool, float* conv_pool, void* stream) {
+    NvtxRange nvtx_range("gdn_copy_slots");
+    int st = check_pool(dims, pool_rows, state_pool, conv_pool);
+    if (st != GDN_OK) return st;
+    if (n < 0) return GDN_ERR_INVALID_ARG;
+    if (n == 0) return GDN_OK;
+    if (src_host == nullptr) return GDN_ERR_INVALID_ARG;
+    try {
+        if ((st = check_slots(dst_host, n, pool_rows)) != GDN_OK) return st;
+        std::vector<RowPair> pairs((size_t)n);
+        for (int32_t i = 0; i < n; ++i) {
+            if (src_host[i] < -1 || src_host[i] >= pool_rows) return GDN_ERR_INVALID_ARG;
+            pairs[i] = RowPair{src_host[i], dst_host[i]};
+        }
+        if ((st = check_device()) != GDN_OK) return st;
+        return pool_launch(dims, std::move(pairs), pool_rows, state_pool, conv_pool,
+                           static_cast<cudaStream_t>(stream));
+    } catch (const std::bad_alloc&) {
+        return GDN_ERR_HOST_MEMORY;
+    }
+}
+
+int gdn_compact_slots(const gdn_dims* dims, int32_t pool_rows, const uint8_t* live_host, int32_t clear,
+                      float* state_pool, float* conv_pool, int32_t* remap_host, void* stream) {
+    NvtxRange nvtx_range("gdn_compact_slots");
+    int st = check_pool(dims, pool_rows, state_pool, conv_pool);
+    if (st != GDN_OK) return st;
+    if (pool_rows == 0) return GDN_OK;
+    if (live_host == nullptr || remap_host == nullptr) return GDN_ERR_INVALID_ARG;
+    if ((st = check_device()) != GDN_OK) return st;
+    int32_t nlive = 0;
+    for (int32_t i = 0; i < pool_rows; ++i) nlive += live_host[i] != 0;
+    try {
+        std::vector<RowPair> pairs;
+        int32_t hole = 0;
+        for (int32_t i = 0; i < pool_rows; ++i) {
+            remap_host[i] = live_host[i] ? i : -1;
+            if (live_host[i] && i >= nlive) {
+                while (live_host[hole]) ++hole;
+                remap_host[i] = hole;
+                pairs.push_back(RowPair{i, hole++});
+            }
+            if (clear && i >= nlive) pairs.push_back(RowPair{-1, i});
+        }
+        return pool_launch(dims, std::move(pairs), pool_rows, state_pool, conv_pool,
+                           static_cast<cudaStream_t>(stream));
+    } catch (const std::bad_alloc&) {
+        return GDN_ERR_HOST_MEMORY;
+    }
+}
 
 }  // extern "C"

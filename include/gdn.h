@@ -59,7 +59,8 @@ enum gdn_status {
     GDN_ERR_UNSUPPORTED = -2, /* head_dim != 128, conv_width != 4, Vh % Kh != 0, Vh/Kh > 8, not sm_100 */
     GDN_ERR_CUDA = -3,        /* a CUDA runtime / driver call failed */
     GDN_ERR_WORKSPACE = -4,   /* workspace missing or smaller than the *_workspace_size query */
-    GDN_ERR_TIMEOUT = -5      /* a bounded device-side wait expired (see gdn_last_device_error) */
+    GDN_ERR_TIMEOUT = -5,     /* a bounded device-side wait expired (see gdn_last_device_error) */
+    GDN_ERR_HOST_MEMORY = -6  /* the call's host-side tables could not be allocated */
 };
 
 typedef struct gdn_dims {
@@ -241,6 +242,35 @@ int gdn_prefill_varlen_slots(const gdn_dims* dims, const gdn_weights* w, int32_t
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Moves of whole pool rows (the slot pool above): row r of both pools, its
+ * state and its history, moves together.  Host tables only: they are checked
+ * and turned into the launch's parameters during the call, and may be reused
+ * or freed when it returns; captured into a graph, a call keeps the tables of
+ * the capture.  No workspace.  GDN_ERR_INVALID_ARG before anything is enqueued
+ * for a row outside the pool.
+ *
+ * gdn_copy_slots: pool row dst[i] becomes what row src[i] held before the
+ * call, or zero where src[i] is -1, for the n pairs at once: every read comes
+ * before every write, so a row may be read by several pairs (fork), overwritten
+ * and read (reordering, swaps and cycles), or kept (src[i] == dst[i]).  No dst
+ * twice (GDN_ERR_INVALID_ARG).  Each row that is read is read once, each row
+ * that changes is written once, and pool rows that no dst names are not
+ * touched.  Pairs that form one connected set (linked by shared rows) in which
+ * a source is overwritten may number 512 at most, else GDN_ERR_UNSUPPORTED.
+ *
+ * gdn_compact_slots: the rows with live_host[r] != 0 move into the first
+ * n_live rows: live rows before n_live stay, those behind fill the free rows
+ * before n_live in ascending order.  remap_host[r] (written during the call)
+ * is the new row of old row r, -1 if it was not live.  clear != 0: the rows
+ * from n_live on become zero (ready for new sequences); 0: they keep what
+ * they held.
+ */
+int gdn_copy_slots(const gdn_dims* dims, int32_t n, const int32_t* src_host, const int32_t* dst_host,
+                   int32_t pool_rows, float* state_pool, float* conv_pool, void* stream);
+int gdn_compact_slots(const gdn_dims* dims, int32_t pool_rows, const uint8_t* live_host, int32_t clear,
+                      float* state_pool, float* conv_pool, int32_t* remap_host, void* stream);
+
+/*
  * The projections around the mixer as bf16 tensor-core GEMMs with f32
  * accumulation and one rounding to bf16 (Qwen/Qwen3.8-27B architecture page,
  * module tree of `linear_attn`: in_proj_qkv 10240x5120, in_proj_z 6144x5120,
@@ -260,6 +290,58 @@ int gdn_in_proj(const gdn_dims* dims, int32_t T, int32_t hidden, const uint16_t*
                 uint16_t* qkv, uint16_t* z, uint16_t* b, uint16_t* a, void* stream);
 int gdn_out_proj(const gdn_dims* dims, int32_t T, int32_t hidden, const uint16_t* y, const uint16_t* w_out,
                  uint16_t* out, void* stream);
+
+/*
+ * Microscaled 4-bit operands (E2M1 codes: +-0, .5, 1, 1.5, 2, 3, 4, 6).  An
+ * element of a row of K stands for
+ *     value[r][k] = code[r][k] * scale[r][k / B] * row_scale[r]
+ *   GDN_NVFP4: B = 16, E4M3 scales; row_scale[r] is the least power of two (at
+ *     least 2^-100) that keeps the row's scales within E4M3, amax_r <= 448 * 6 *
+ *     row_scale[r]; scale = amax_block / (6 row_scale) and code = x / (scale
+ *     row_scale), both rounded to nearest even.
+ *   GDN_MXFP4: B = 32, power-of-two scales (exponent + 127 in a byte): scale =
+ *     2^(floor(log2 amax_block) - 2), code = x / scale rounded to nearest even
+ *     and saturated; row_scale[r] = 1.
+ * A row that holds an infinity or a NaN gets row_scale NaN: all its values are
+ * NaN, other rows are not affected.  Weights quantised elsewhere fit in when
+ * laid out so, with any finite row scales (a tensor-wide scale repeated).
+ *   codes     uint8 [rows][K/2], element 2i in the low nibble of byte i
+ *   scales    uint8, gdn_quant_scale_bytes(format, rows, K) bytes: tiles of
+ *             128 rows x 4 blocks of 512 bytes, tiles of a row block next to
+ *             each other; in a tile, row r and block b at
+ *             (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.  Bytes of rows past the
+ *             last in its tile are neither written nor used.
+ *   row_scale f32 [rows]
+ * K is a multiple of 64 (GDN_ERR_UNSUPPORTED otherwise), codes, scales, x and
+ * out 16-byte aligned.  rows = 0 is a legal no-op.  The value is exact in bf16
+ * unless it leaves bf16's range: gdn_dequantize(gdn_quantize(x)) returns the
+ * rounded values without a further rounding.
+ */
+enum gdn_quant_format { GDN_NVFP4 = 0, GDN_MXFP4 = 1 };
+size_t gdn_quant_scale_bytes(int32_t format, int32_t rows, int32_t K);
+int gdn_quantize(int32_t format, int32_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
+                 float* row_scale, void* stream);
+int gdn_dequantize(int32_t format, int32_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales,
+                   const float* row_scale, uint16_t* out, void* stream);
+
+/*
+ * gdn_in_proj and gdn_out_proj on 4-bit operands: the weights are held
+ * quantised (codes, scales and row scales of [N][K], N and K as in the bf16
+ * projections), the tokens x (y) bf16 [T][K] are quantised row by row in the
+ * same format inside the call, each token by itself.  The block-scaled
+ * products are summed in f32, multiplied by the two row scales and rounded once
+ * to bf16.  Outputs as for gdn_in_proj / gdn_out_proj, 16-byte aligned.
+ * workspace: gdn_proj_quant_workspace_size(format, T, K) bytes (the quantised
+ * tokens), 16-byte aligned.  K a multiple of 64 (GDN_ERR_UNSUPPORTED
+ * otherwise).  T = 0 is a legal no-op.  Asynchronous on `stream`.
+ */
+size_t gdn_proj_quant_workspace_size(int32_t format, int32_t T, int32_t K);
+int gdn_in_proj_quant(const gdn_dims* dims, int32_t format, int32_t T, int32_t hidden, const uint16_t* x,
+                      const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scale, uint16_t* qkv,
+                      uint16_t* z, uint16_t* b, uint16_t* a, void* workspace, size_t workspace_bytes, void* stream);
+int gdn_out_proj_quant(const gdn_dims* dims, int32_t format, int32_t T, int32_t hidden, const uint16_t* y,
+                       const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scale, uint16_t* out,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Dense prefill from the layer's hidden states: gdn_in_proj and gdn_prefill
