@@ -1310,6 +1310,37 @@ bool make_code_map(CUtensorMap* m, const uint8_t* base, int32_t K, int64_t rows,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The scale tiles as rows of 512 bytes, `stage` of them per box.
+bool make_scale_map(CUtensorMap* m, const uint8_t* base, int64_t tiles, uint32_t stage) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {quant::kTileBytes / 4, (cuuint64_t)tiles};
+    cuuint64_t strides[1] = {quant::kTileBytes};
+    cuuint32_t box[2] = {quant::kTileBytes / 4, stage};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT>
+int qproj_pairs(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
+    CUtensorMap mW, mX, mSw, mSx;
+    const int stage = qproj::kTilesPerStage(FMT);
+    if (!make_code_map(&mW, cw, p.K, p.N, 128) || !make_code_map(&mX, cx, p.K, p.T, 128) ||
+        !make_scale_map(&mSw, p.sw, (int64_t)((p.N + 127) / 128) * p.tiles, stage) ||
+        !make_scale_map(&mSx, p.sx, (int64_t)((p.T + 127) / 128) * p.tiles, stage))
+        return GDN_ERR_CUDA;
+    auto kernel = gdn_qproj_pair_kernel<FMT>;
+    int st = smem_optin(reinterpret_cast<const void*>(kernel), qproj::duo::SMEM_BYTES);
+    if (st != GDN_OK) return st;
+    const int64_t ntiles = (int64_t)((p.T + qproj::duo::kTileM - 1) / qproj::duo::kTileM) *
+                           ((p.N + qproj::duo::kTileN - 1) / qproj::duo::kTileN);
+    const int pairs = (int)(ntiles < nsm / 2 ? ntiles : nsm / 2);
+    kernel<<<2 * pairs, qproj::duo::kDuoThreads, qproj::duo::SMEM_BYTES, stream>>>(mW, mX, mSw, mSx, p);
+    return cuda_status(cudaGetLastError());
+}
+
 template <int FMT, int BN>
 int qproj_tiles(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
     CUtensorMap mW, mX;
@@ -1327,7 +1358,12 @@ template <int FMT>
 int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
     if (p.T <= 16) return qproj_tiles<FMT, 16>(cx, cw, p, stream);
     if (p.T <= 64) return qproj_tiles<FMT, 64>(cx, cw, p, stream);
-    return qproj_tiles<FMT, 128>(cx, cw, p, stream);
+    if (p.T <= 128) return qproj_tiles<FMT, 128>(cx, cw, p, stream);
+    int dev = 0, nsm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return qproj_pairs<FMT>(cx, cw, p, nsm, stream);
 }
 
 // Workspace of a 4-bit projection: the quantised tokens.

@@ -16,6 +16,17 @@ constexpr int BK = 256;                 // elements of K per stage: 128 bytes, o
 constexpr int kMmaK = 64;               // elements of K per tcgen05.mma
 __host__ __device__ constexpr int kTilesPerStage(int fmt) { return BK / (4 * quant::block_of(fmt)); }  // scale tiles per 128 rows: 4 or 2
 
+// One lane of the (converged) warp.  The loads and products are issued from code that the whole warp runs,
+// inside one elected block per stage with every descriptor formed from warp-uniform values: the operands
+// then stay in uniform registers.  Issued by a lane picked with `lane == 0`, from loops, a product took
+// about 73 issue cycles and a scale copy 60; so, 4 products and 12 copies take under 300 (M = 256, N = 256:
+// 512 of tensor time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r != 0;
+}
+
 // Instruction descriptor of the block-scaled 4-bit kinds: E2M1 operands, both K-major, f32 sums;
 // scale type E4M3 (0) or power of two (1).  The scale ids (bits 4-5 and 29-30: which bytes of a
 // scale word a product reads) are or'ed in.
@@ -63,12 +74,23 @@ struct Params {
     GemmSegment seg[4];
 };
 
-__device__ __forceinline__ uint16_t* output_at(const Params& p, int n, int t) {
-    int sg = 0;
+// The segment of feature n, by selects (indexing the parameter array would copy it to local memory).
+__device__ __forceinline__ GemmSegment segment_of(const Params& p, int n, int& end) {
+    GemmSegment g = p.seg[0];
+    end = p.nseg > 1 ? p.seg[1].col0 : p.N;
 #pragma unroll
     for (int i = 1; i < 4; ++i)
-        if (i < p.nseg && n >= p.seg[i].col0) sg = i;
-    return p.seg[sg].dst + (size_t)t * p.seg[sg].ld + (n - p.seg[sg].col0);
+        if (i < p.nseg && n >= p.seg[i].col0) {
+            g = p.seg[i];
+            end = i + 1 < p.nseg ? p.seg[i < 3 ? i + 1 : 3].col0 : p.N;
+        }
+    return g;
+}
+
+__device__ __forceinline__ uint16_t* output_at(const Params& p, int n, int t) {
+    int end;
+    const GemmSegment g = segment_of(p, n, end);
+    return g.dst + (size_t)t * g.ld + (n - g.col0);
 }
 
 constexpr int BM = 128;                              // features per tile (rows of the A operand)
@@ -211,6 +233,295 @@ __global__ void __launch_bounds__(qproj::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tbase, C::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------- many tokens: pairs of SMs
+namespace qproj {
+namespace duo {
+constexpr int kTileM = 256, kTileN = 256;             // tokens x features of a pair's tile
+constexpr uint32_t kCodeBytes = 128 * BK / 2;         // one CTA's 128 tokens, or its 128 of the features
+constexpr int kStages = 5;
+constexpr uint32_t STAGE_BYTES = 2 * kCodeBytes + 3 * S_BYTES;  // + scales of 128 tokens and 256 features
+constexpr uint32_t OFF_MISC = kStages * STAGE_BYTES;
+constexpr uint32_t OFF_GW = OFF_MISC + 256;           // the tile's feature row scales, two buffers
+constexpr uint32_t SMEM_BYTES = OFF_GW + 2 * kTileN * 4 + 1024;
+constexpr int kDuoThreads = 192;                      // warp 0 loads, warp 1 products, warps 2-5 epilogue
+// Tensor memory: two accumulators of 256 columns that share columns [kAcc1, 256), and two buffers of
+// scales behind them (16 columns of token scales, 32 of feature scales each).
+constexpr uint32_t kAcc1 = 160, kScales = kAcc1 + kTileN, kScaleCols = 48;
+static_assert(kScales + 2 * kScaleCols <= 512, "tensor memory");
+constexpr int kWalkM = 16;                            // M tiles swept across all N tiles (the bf16 GEMM's walk)
+}  // namespace duo
+
+// Address of this variable's counterpart in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+    return r;
+}
+
+// TMA load into this CTA that completes bytes of a barrier in either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs when the pair's products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb,
+                                                uint32_t accumulate) {
+    if constexpr (FMT == quant::kNvfp4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+}
+
+// 32 results of one token (features c0 ..) into the output segments.
+__device__ __forceinline__ void store_row32(const Params& p, int t, int c0, const float (&v)[32]) {
+    int end;
+    const GemmSegment g = segment_of(p, c0, end);
+    uint16_t* dst = g.dst + (size_t)t * g.ld + (c0 - g.col0);
+    if (c0 + 32 <= end && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint4 pk;
+            pk.x = pack_bf16x2(v[8 * e + 0], v[8 * e + 1]);
+            pk.y = pack_bf16x2(v[8 * e + 2], v[8 * e + 3]);
+            pk.z = pack_bf16x2(v[8 * e + 4], v[8 * e + 5]);
+            pk.w = pack_bf16x2(v[8 * e + 6], v[8 * e + 7]);
+            reinterpret_cast<uint4*>(dst)[e] = pk;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e)  // segment boundaries, the last columns, rows off 16 bytes
+        if (c0 + e < p.N) *output_at(p, c0 + e, t) = float_to_bf16_bits(v[e]);
+}
+
+}  // namespace qproj
+
+// Clusters of two CTAs walk 256 x 256 tiles of tokens x features: each CTA holds 128 tokens' rows and
+// 128 of the features' rows in shared memory and the sums of its 128 tokens x 256 features in tensor
+// memory; the products (cta_group::2, M = 256, N = 256) read both CTAs' shared memory, so each SM loads
+// half the weights of the tile.  Rank 0 issues the products; both CTAs load and run their epilogue.
+template <int FMT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThreads, 1)
+    gdn_qproj_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                          const __grid_constant__ CUtensorMap tmSw, const __grid_constant__ CUtensorMap tmSx,
+                          const qproj::Params p) {
+    using namespace qproj;
+    using namespace qproj::duo;
+    constexpr int kTiles = kTilesPerStage(FMT);
+    constexpr uint32_t kScaleBytes = kTiles * quant::kTileBytes;  // scale bytes of 128 rows and a stage
+    constexpr uint32_t TX = 2 * (2 * kCodeBytes + 3 * kScaleBytes);
+    constexpr uint32_t ID = idesc(FMT, kTileM, kTileN);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_MISC);  // rank 0: both CTAs' loads of a stage
+    uint64_t* empty = full + kStages;                               // the stage's products are done
+    uint64_t* acc_full = empty + kStages;                           // [2] a tile's sums are complete
+    uint64_t* acc_free = acc_full + 2;                              // rank 0: the shared columns are drained
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + OFF_MISC + 128);
+    float* s_gw = reinterpret_cast<float*>(smem + OFF_GW);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int tiles_m = (p.T + kTileM - 1) / kTileM, tiles_n = (p.N + kTileN - 1) / kTileN;
+    const int ntiles = tiles_m * tiles_n, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int ksteps = (p.K + BK - 1) / BK;
+    auto coords = [&](int t, int& tm, int& tn) {
+        const int per_group = kWalkM * tiles_n;
+        const int g = t / per_group, r = t - g * per_group;
+        const int gm = min(kWalkM, tiles_m - g * kWalkM);
+        tn = r / gm;
+        tm = g * kWalkM + (r - tn * gm);
+    };
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&acc_full[0], 1);
+        mbar_init(&acc_full[1], 1);
+        mbar_init(acc_free, 8);  // the epilogue warps of both CTAs
+        fence_barrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmSw);
+        prefetch_tensormap(&tmSx);
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tbase = *s_tmem;
+    bool broken = false;
+    auto wait1 = [&](uint64_t* bar, uint32_t parity, int code) {
+        if (!broken && !mbar_wait(bar, parity)) {
+            broken = true;
+            record_error(code);
+        }
+    };
+
+    if (warp == 0) {
+        // ---------------- loads: this CTA's rows; the bytes of both CTAs complete on rank 0's barrier
+        uint32_t q = 0;
+        for (int t = first; t < ntiles && !broken; t += step) {
+            int tm, tn;
+            coords(t, tm, tn);
+            const int m0 = tm * kTileM + 128 * rank, n0 = tn * kTileN + 128 * rank;
+            const int yx = (m0 >> 7) * p.tiles, yw = 2 * tn * p.tiles;
+            for (int ks = 0; ks < ksteps; ++ks, ++q) {
+                const int s = q % kStages;
+                if (q >= kStages) wait1(&empty[s], ((q / kStages) - 1) & 1, kErrTimeoutTma);
+                if (broken) break;
+                uint8_t* st = smem + s * STAGE_BYTES;
+                uint8_t* sc = st + 2 * kCodeBytes;
+                const uint32_t bar = cluster_addr(&full[s], 0);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], TX);
+                    tma_load_2d_pair(st, &tmX, ks * (BK / 2), m0, bar);
+                    tma_load_2d_pair(st + kCodeBytes, &tmW, ks * (BK / 2), n0, bar);
+                    tma_load_2d_pair(sc, &tmSx, 0, yx + ks * kTiles, bar);
+                    tma_load_2d_pair(sc + S_BYTES, &tmSw, 0, yw + ks * kTiles, bar);
+                    tma_load_2d_pair(sc + 2 * S_BYTES, &tmSw, 0, yw + p.tiles + ks * kTiles, bar);
+                }
+                __syncwarp();
+            }
+        }
+        // no copy is in flight when the pair exits
+        if (rank == 0)
+            for (uint32_t i = q > kStages ? q - kStages : 0; i < q; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
+    } else if (warp == 1) {
+        // ---------------- products (rank 0)
+        if (rank == 0) {
+            const uint64_t kDesc = sw128_desc(0, 16, 1024), sDesc = scale_desc(0);
+            uint32_t q = 0, it = 0;
+            for (int t = first; t < ntiles && !broken; t += step, ++it) {
+                // the accumulators share columns: those of the previous tile are drained first (and with
+                // them, in order, everything of the tile before it)
+                if (it >= 1 && !broken && !mbar_wait_cluster(acc_free, (it - 1) & 1)) {
+                    broken = true;
+                    record_error(kErrTimeoutMma);
+                }
+                tc_fence_after();
+                const uint32_t d = tbase + ((it & 1) ? kAcc1 : 0);
+                for (int ks = 0; ks < ksteps; ++ks, ++q) {
+                    const int s = q % kStages;
+                    wait1(&full[s], (q / kStages) & 1, kErrTimeoutTma);
+                    // the scale buffer's last readers, two stages back, are done
+                    if (q >= 2) wait1(&empty[(q - 2) % kStages], ((q - 2) / kStages) & 1, kErrTimeoutMma);
+                    if (broken) break;
+                    tc_fence_after();
+                    const uint32_t aX = sbase + s * STAGE_BYTES, aS = aX + 2 * kCodeBytes;
+                    const uint64_t dX = desc_at(kDesc, aX), dW = desc_at(kDesc, aX + kCodeBytes), dS = desc_at(sDesc, aS);
+                    const uint32_t cX = tbase + kScales + (q & 1) * kScaleCols, cW = cX + 16;
+                    const int nk = min(BK / kMmaK, (p.K - ks * BK) / kMmaK);
+                    const uint32_t more = ks > 0;
+                    if (elect_one()) {
+                        // (at the end of K some tiles hold other rows' scales: no product reads them)
+#pragma unroll
+                        for (int i = 0; i < kTiles; ++i) {
+                            copy_scales_pair(cX + 4 * i, dS + 32 * i);
+                            copy_scales_pair(cW + 8 * i, dS + (S_BYTES >> 4) + 32 * i);
+                            copy_scales_pair(cW + 8 * i + 4, dS + (2 * S_BYTES >> 4) + 32 * i);
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < BK / kMmaK; ++kk) {
+                            constexpr bool nv = FMT == quant::kNvfp4;
+                            const int tile = nv ? kk : kk >> 1;
+                            if (kk < nk)
+                                mma_scaled_pair<FMT>(d, dX + 2 * kk, dW + 2 * kk, nv ? ID : ID | scale_id(2 * (kk & 1)),
+                                                     cX + 4 * tile, cW + 8 * tile, kk > 0 ? 1u : more);
+                        }
+                        commit_pair(&empty[s]);
+                        if (ks + 1 == ksteps) commit_pair(&acc_full[it & 1]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        // ---------------- epilogue: this CTA's 128 tokens
+        const int q4 = warp & 3, et = tid - 64;
+        const uint32_t tl = static_cast<uint32_t>(32 * q4) << 16;
+        const uint32_t free_bar = cluster_addr(acc_free, 0);
+        uint32_t it = 0;
+        for (int t = first; t < ntiles; t += step, ++it) {
+            int tm, tn;
+            coords(t, tm, tn);
+            const int row = tm * kTileM + 128 * rank + 32 * q4 + lane, n0 = tn * kTileN;
+            float* gw = s_gw + (it & 1) * kTileN;
+            for (int i = et; i < kTileN; i += 128) gw[i] = n0 + i < p.N ? __ldg(p.gw + n0 + i) : 0.0f;
+            const float gx = row < p.T ? __ldg(p.gx + row) : 0.0f;
+            named_barrier_sync(1, 128);
+            wait1(&acc_full[it & 1], (it >> 1) & 1, kErrTimeoutMma);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t acc = tbase + tl + ((it & 1) ? kAcc1 : 0);
+            // the shared columns first, into registers, and the next tile's products may start
+            const int shared0 = (it & 1) ? 0 : kAcc1;  // the accumulator's column of tensor-memory column kAcc1
+            auto emit = [&](int c, float(&v)[32]) {
+                if (row < p.T && n0 + c < p.N) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] *= gx * gw[c + e];
+                    store_row32(p, row, n0 + c, v);
+                }
+                __syncwarp();
+            };
+            float v0[32], v1[32], v2[32];
+            tmem_ld32(acc + shared0, v0);
+            tmem_ld32(acc + shared0 + 32, v1);
+            tmem_ld32(acc + shared0 + 64, v2);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(free_bar) : "memory");
+            emit(shared0, v0);
+            emit(shared0 + 32, v1);
+            emit(shared0 + 64, v2);
+            const int rest0 = (it & 1) ? 96 : 0;
+#pragma unroll 1
+            for (int j = 0; j < 5; ++j) {
+                tmem_ld32(acc + rest0 + 32 * j, v0);
+                tmem_ld_wait();
+                emit(rest0 + 32 * j, v0);
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512u) : "memory");
 }
 
 }  // namespace gdn
