@@ -244,7 +244,9 @@ constexpr int kStages = 5;
 constexpr uint32_t STAGE_BYTES = 2 * kCodeBytes + 3 * S_BYTES;  // + scales of 128 tokens and 256 features
 constexpr uint32_t OFF_MISC = kStages * STAGE_BYTES;
 constexpr uint32_t OFF_GW = OFF_MISC + 256;           // the tile's feature row scales, two buffers
-constexpr uint32_t SMEM_BYTES = OFF_GW + 2 * kTileN * 4 + 1024;
+constexpr uint32_t kOutBytes = 32 * 128;              // a warp's 32 tokens x 64 features on their way out
+constexpr uint32_t OFF_OUT = OFF_GW + 2 * kTileN * 4;
+constexpr uint32_t SMEM_BYTES = OFF_OUT + 4 * kOutBytes + 1024;
 constexpr int kDuoThreads = 192;                      // warp 0 loads, warp 1 products, warps 2-5 epilogue
 // Tensor memory: two accumulators of 256 columns that share columns [kAcc1, 256), and two buffers of
 // scales behind them (16 columns of token scales, 32 of feature scales each).
@@ -299,26 +301,47 @@ __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t
             : "memory");
 }
 
-// 32 results of one token (features c0 ..) into the output segments.
-__device__ __forceinline__ void store_row32(const Params& p, int t, int c0, const float (&v)[32]) {
+// 32 sums of one token (features c0 ..) times the row scales, as bf16 pairs.
+__device__ __forceinline__ void scale_pack32(const float (&v)[32], float gx, const float* gw, uint32_t (&o)[16]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float4 g = reinterpret_cast<const float4*>(gw)[e];
+        o[2 * e] = pack_bf16x2(v[4 * e] * (gx * g.x), v[4 * e + 1] * (gx * g.y));
+        o[2 * e + 1] = pack_bf16x2(v[4 * e + 2] * (gx * g.z), v[4 * e + 3] * (gx * g.w));
+    }
+}
+
+// A warp's 32 tokens x 64 features into the output segments: lane l holds token t0 + l, features c0 .. c0 + 63
+// as bf16 pairs.  Inside one segment with 16-byte rows they go through shared memory (32 rows of 128 bytes,
+// 16-byte chunks swizzled by row: no bank conflicts), so that eight lanes store one token's 128 contiguous
+// bytes (stored by each lane straight to its own row, the output cost 37 of 322 us at 8192 x 16480 x 5120).
+__device__ __forceinline__ void store_tile32x64(const Params& p, int t0, int c0, const uint32_t (&lo)[16],
+                                                const uint32_t (&hi)[16], uint8_t* stage, int lane) {
     int end;
     const GemmSegment g = segment_of(p, c0, end);
-    uint16_t* dst = g.dst + (size_t)t * g.ld + (c0 - g.col0);
-    if (c0 + 32 <= end && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+    const int col = c0 - g.col0;
+    if (c0 + 64 <= end && ((col | g.ld) & 7) == 0) {  // (segments start on 16 bytes)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint4 pk;
-            pk.x = pack_bf16x2(v[8 * e + 0], v[8 * e + 1]);
-            pk.y = pack_bf16x2(v[8 * e + 2], v[8 * e + 3]);
-            pk.z = pack_bf16x2(v[8 * e + 4], v[8 * e + 5]);
-            pk.w = pack_bf16x2(v[8 * e + 6], v[8 * e + 7]);
-            reinterpret_cast<uint4*>(dst)[e] = pk;
+        for (int c = 0; c < 4; ++c) {
+            *reinterpret_cast<uint4*>(stage + sw128_chunk(lane, c)) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            *reinterpret_cast<uint4*>(stage + sw128_chunk(lane, 4 + c)) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
         }
-        return;
-    }
+        __syncwarp();
+        uint16_t* dst = g.dst + (size_t)t0 * g.ld + col + (lane & 7) * 8;
 #pragma unroll
-    for (int e = 0; e < 32; ++e)  // segment boundaries, the last columns, rows off 16 bytes
-        if (c0 + e < p.N) *output_at(p, c0 + e, t) = float_to_bf16_bits(v[e]);
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128_chunk(r, lane & 7));
+            if (t0 + r < p.T) *reinterpret_cast<uint4*>(dst + (size_t)r * g.ld) = v;
+        }
+    } else if (t0 + lane < p.T) {  // segment boundaries, the last features, rows off 16 bytes
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+            const uint32_t w = e < 32 ? lo[(e & 31) >> 1] : hi[(e & 31) >> 1];
+            if (c0 + e < p.N) *output_at(p, c0 + e, t0 + lane) = static_cast<uint16_t>(e & 1 ? w >> 16 : w);
+        }
+    }
+    __syncwarp();
 }
 
 }  // namespace qproj
@@ -424,26 +447,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
         // ---------------- products (rank 0)
         if (rank == 0) {
             const uint64_t kDesc = sw128_desc(0, 16, 1024), sDesc = scale_desc(0);
-            uint32_t q = 0, it = 0;
+            // stage s of the ring, its phase; the stage two back, its phase
+            uint32_t s = 0, ph = 0, s2 = kStages - 2, ph2 = 1, it = 0, cS = tbase + kScales;
+            bool primed = false;  // two stages have been issued
             for (int t = first; t < ntiles && !broken; t += step, ++it) {
                 // the accumulators share columns: those of the previous tile are drained first (and with
                 // them, in order, everything of the tile before it)
-                if (it >= 1 && !broken && !mbar_wait_cluster(acc_free, (it - 1) & 1)) {
+                if (it >= 1 && !mbar_wait_cluster(acc_free, (it - 1) & 1)) {
                     broken = true;
                     record_error(kErrTimeoutMma);
                 }
                 tc_fence_after();
                 const uint32_t d = tbase + ((it & 1) ? kAcc1 : 0);
-                for (int ks = 0; ks < ksteps; ++ks, ++q) {
-                    const int s = q % kStages;
-                    wait1(&full[s], (q / kStages) & 1, kErrTimeoutTma);
-                    // the scale buffer's last readers, two stages back, are done
-                    if (q >= 2) wait1(&empty[(q - 2) % kStages], ((q - 2) / kStages) & 1, kErrTimeoutMma);
+                for (int ks = 0; ks < ksteps; ++ks) {
+                    // the stage is loaded, and the scale buffer's last readers, two stages back, are done (both
+                    // asked at once: a wait that succeeds costs about 80 cycles)
+                    const bool loaded = mbar_try_wait(smem_u32(&full[s]), ph);
+                    const bool done2 = mbar_try_wait(smem_u32(&empty[s2]), ph2);
+                    if (!loaded) wait1(&full[s], ph, kErrTimeoutTma);
+                    if (!done2 && primed) wait1(&empty[s2], ph2, kErrTimeoutMma);
                     if (broken) break;
                     tc_fence_after();
                     const uint32_t aX = sbase + s * STAGE_BYTES, aS = aX + 2 * kCodeBytes;
                     const uint64_t dX = desc_at(kDesc, aX), dW = desc_at(kDesc, aX + kCodeBytes), dS = desc_at(sDesc, aS);
-                    const uint32_t cX = tbase + kScales + (q & 1) * kScaleCols, cW = cX + 16;
+                    const uint32_t cX = cS, cW = cX + 16;
                     const int nk = min(BK / kMmaK, (p.K - ks * BK) / kMmaK);
                     const uint32_t more = ks > 0;
                     if (elect_one()) {
@@ -466,6 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
                         if (ks + 1 == ksteps) commit_pair(&acc_full[it & 1]);
                     }
                     __syncwarp();
+                    cS = cS == tbase + kScales ? cS + kScaleCols : tbase + kScales;
+                    if (++s == kStages) s = 0, ph ^= 1;
+                    if (++s2 == kStages) s2 = 0, ph2 ^= 1, primed = true;
                 }
             }
         }
@@ -487,16 +517,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             __syncwarp();
             tc_fence_after();
             const uint32_t acc = tbase + tl + ((it & 1) ? kAcc1 : 0);
-            // the shared columns first, into registers, and the next tile's products may start
-            const int shared0 = (it & 1) ? 0 : kAcc1;  // the accumulator's column of tensor-memory column kAcc1
-            auto emit = [&](int c, float(&v)[32]) {
-                if (row < p.T && n0 + c < p.N) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] *= gx * gw[c + e];
-                    store_row32(p, row, n0 + c, v);
-                }
-                __syncwarp();
-            };
+            // the shared columns first, into registers, and the next tile's products may start: columns
+            // 160 .. 255 of the first accumulator, 0 .. 95 of the second
+            const int shared0 = (it & 1) ? 0 : kAcc1;
             float v0[32], v1[32], v2[32];
             tmem_ld32(acc + shared0, v0);
             tmem_ld32(acc + shared0 + 32, v1);
@@ -504,17 +527,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
+            // relaxed: the columns are in registers (tmem_ld_wait), there is nothing else to publish; a release
+            // at cluster scope would wait for the previous tile's output stores (about 1,300 cycles a tile)
             if (lane == 0)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(free_bar) : "memory");
-            emit(shared0, v0);
-            emit(shared0 + 32, v1);
-            emit(shared0 + 64, v2);
-            const int rest0 = (it & 1) ? 96 : 0;
-#pragma unroll 1
-            for (int j = 0; j < 5; ++j) {
-                tmem_ld32(acc + rest0 + 32 * j, v0);
+                asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(free_bar) : "memory");
+            uint8_t* stage = smem + OFF_OUT + (warp - 2) * kOutBytes;
+            const int t0 = row - lane;
+            uint32_t lo[16], hi[16];
+            auto from_tmem = [&](int c, uint32_t(&o)[16]) {
+                tmem_ld32(acc + c, v0);
                 tmem_ld_wait();
-                emit(rest0 + 32 * j, v0);
+                scale_pack32(v0, gx, gw + c, o);
+            };
+            auto emit = [&](int c) {
+                if (n0 + c < p.N) store_tile32x64(p, t0, n0 + c, lo, hi, stage, lane);
+            };
+            const bool second = (it & 1) != 0;  // the accumulator with the shared columns at its start
+            if (second) {
+                scale_pack32(v0, gx, gw, lo);
+                scale_pack32(v1, gx, gw + 32, hi);
+                emit(0);
+                scale_pack32(v2, gx, gw + 64, lo);
+                from_tmem(96, hi);
+                emit(64);
+            } else {
+                scale_pack32(v1, gx, gw + 192, lo);
+                scale_pack32(v2, gx, gw + 224, hi);
+                emit(192);
+                scale_pack32(v0, gx, gw + 160, hi);
+                from_tmem(128, lo);
+                emit(128);
+            }
+#pragma unroll 1
+            for (int c = second ? 128 : 0; c < (second ? 256 : 128); c += 64) {
+                from_tmem(c, lo);
+                from_tmem(c + 32, hi);
+                emit(c);
             }
         }
     }
