@@ -1284,16 +1284,33 @@ size_t quant_scale_bytes(int format, int64_t rows, int K) {
     return (size_t)((rows + 127) / 128) * quant::scale_tiles(format, K) * quant::kTileBytes;
 }
 
-int quantize_launch(int format, int32_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
-                    float* row_scale, cudaStream_t stream) {
-    quant::Params p{x, codes, scales, row_scale, rows, K, quant::scale_tiles(format, K)};
-    // threads per row: one unit of 16 elements each, up to 512 (then two or more); at least 256 per CTA
+// Launch shape of the row kernels: one unit of 16 elements per thread up to 512 threads a row (then two or
+// more), at least 256 threads a CTA, as many CTAs as the device holds at 2048 threads an SM.
+int quant_shape(int32_t rows, int32_t K, dim3* grid, dim3* block) {
+    int dev = 0, nsm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return GDN_ERR_CUDA;
     const int units = K / quant::kUnit;
     const int gx = units >= quant::kMaxGroup ? quant::kMaxGroup : (units + 31) / 32 * 32;
     const int gy = gx >= 256 ? 1 : 256 / gx;
-    const dim3 block(gx, gy), grid((rows + gy - 1) / gy);
-    if (format == GDN_NVFP4) gdn_quantize_kernel<quant::kNvfp4><<<grid, block, 0, stream>>>(p);
-    else gdn_quantize_kernel<quant::kMxfp4><<<grid, block, 0, stream>>>(p);
+    const int64_t groups = ((int64_t)rows + gy - 1) / gy, resident = (int64_t)nsm * (2048 / (gx * gy));
+    *block = dim3(gx, gy);
+    *grid = dim3((unsigned)(groups < resident ? groups : resident));
+    return GDN_OK;
+}
+
+int quantize_launch(int format, int32_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
+                    float* row_scale, cudaStream_t stream) {
+    const quant::Params p{x, codes, scales, row_scale, rows, K, quant::scale_tiles(format, K)};
+    dim3 grid, block;
+    const int st = quant_shape(rows, K, &grid, &block);
+    if (st != GDN_OK) return st;
+    const bool two = K > quant::kMaxGroup * quant::kUnit;
+    auto kernel = format == GDN_NVFP4
+                      ? (two ? gdn_quantize_kernel<quant::kNvfp4, 2> : gdn_quantize_kernel<quant::kNvfp4, 1>)
+                      : (two ? gdn_quantize_kernel<quant::kMxfp4, 2> : gdn_quantize_kernel<quant::kMxfp4, 1>);
+    kernel<<<grid, block, 0, stream>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -1556,14 +1573,10 @@ int gdn_dequantize(int32_t format, int32_t rows, int32_t K, const uint8_t* codes
         return GDN_ERR_INVALID_ARG;
     if ((st = check_device()) != GDN_OK) return st;
     const int tiles = quant::scale_tiles(format, K);
-    const int64_t units = (int64_t)rows * (K / quant::kUnit);
-    const int64_t blocks = (units + 255) / 256;
-    const int grid = (int)(blocks < 65536 ? blocks : 65536);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (format == GDN_NVFP4)
-        gdn_dequantize_kernel<quant::kNvfp4><<<grid, 256, 0, s>>>(codes, scales, row_scale, rows, K, tiles, out);
-    else
-        gdn_dequantize_kernel<quant::kMxfp4><<<grid, 256, 0, s>>>(codes, scales, row_scale, rows, K, tiles, out);
+    dim3 grid, block;
+    if ((st = quant_shape(rows, K, &grid, &block)) != GDN_OK) return st;
+    auto kernel = format == GDN_NVFP4 ? gdn_dequantize_kernel<quant::kNvfp4> : gdn_dequantize_kernel<quant::kMxfp4>;
+    kernel<<<grid, block, 0, static_cast<cudaStream_t>(stream)>>>(codes, scales, row_scale, rows, K, tiles, out);
     return cuda_status(cudaGetLastError());
 }
 

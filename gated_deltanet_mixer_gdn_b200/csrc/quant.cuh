@@ -25,7 +25,6 @@ namespace quant {
 constexpr int kNvfp4 = 0, kMxfp4 = 1;  // enum gdn_quant_format
 constexpr uint32_t kTileBytes = 512;
 constexpr int kUnit = 16;        // elements per thread and step
-constexpr int kHold = 2;         // steps whose elements stay in registers
 constexpr int kMaxGroup = 512;   // threads per row
 
 __host__ __device__ constexpr int block_of(int fmt) { return fmt == kNvfp4 ? 16 : 32; }
@@ -108,7 +107,7 @@ __device__ __forceinline__ void quantize_unit(const uint4& a, const uint4& b, ui
     }
     if constexpr (FMT == kNvfp4) {
         // the reciprocal is rounded, so an exact tie may be off by 2^-23: rounding to 16 significant
-        // bits restores it (x / s is a tie or at least 2^-9 away from one)
+        // bits restores it (x / s is a tie or at least 2^-9 away from one) and keeps the sign of a zero
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float((__float_as_uint(v[i]) + 0x80u) & 0xffffff00u);
     }
@@ -126,108 +125,128 @@ struct Params {
 
 }  // namespace quant
 
-// One row per group of blockDim.x threads (a multiple of 32), blockDim.y rows per CTA.  A thread takes
-// units of 16 elements, blockDim.x units apart; the row is read once while it fits in kHold units per
-// thread (K <= 16384) and twice above.  Bound: HBM (2 bytes read and about 0.57 written per element).
-template <int FMT>
+// One row per group of blockDim.x threads (a multiple of 32), blockDim.y rows per CTA and step; persistent
+// CTAs walk the rows.  A thread takes units of 16 elements, blockDim.x units apart; a row is read once while
+// it fits in kHold units per thread (K <= 16384) and twice above.  The next row's first units are requested
+// before this row's largest magnitude is known, so a row's load latency overlaps the previous row's
+// arithmetic.  kHold is 1 up to K = 8192, else 2 (registers that a short row leaves empty cost occupancy:
+// 16480 x 5120 rows 49 us with 1, 60 us with 2).  Bound: HBM (2 bytes read and about 0.57 written per element).
+template <int FMT, int kHold>
 __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const quant::Params p) {
     using namespace quant;
-    __shared__ uint32_t s_max[kMaxGroup / 32];
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    const bool active = row < p.rows;
-    const int units = p.K / kUnit, step = blockDim.x;
-    const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(active ? row : 0) * p.K);
+    __shared__ uint32_t s_max[2][kMaxGroup / 32];
+    const int units = p.K / kUnit, step = blockDim.x, lane = threadIdx.x & 31;
+    const int groups = (p.rows + blockDim.y - 1) / blockDim.y;  // steps of all CTAs
     uint4 a[kHold], b[kHold];
-    uint32_t bm[kHold];
-    uint32_t rm = 0;
+    auto load = [&](int g) {
+        const int row = g * blockDim.y + threadIdx.y;
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row * p.K);
 #pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-        const int u = threadIdx.x + h * step;
-        a[h] = b[h] = make_uint4(0, 0, 0, 0);
-        if (active && u < units) {
-            a[h] = __ldg(src + 2 * u);
-            b[h] = __ldg(src + 2 * u + 1);
+        for (int h = 0; h < kHold; ++h) {
+            const int u = threadIdx.x + h * step;
+            a[h] = b[h] = make_uint4(0, 0, 0, 0);
+            if (row < p.rows && u < units) {
+                a[h] = __ldg(src + 2 * u);
+                b[h] = __ldg(src + 2 * u + 1);
+            }
         }
-        bm[h] = amax_bits16(a[h], b[h]);
-        rm = max(rm, bm[h]);
-    }
-    for (int u = threadIdx.x + kHold * step; u < units; u += step)
-        if (active) rm = max(rm, amax_bits16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1)));
-    rm = __reduce_max_sync(0xffffffffu, rm);
-    if (step > 32) {  // the row's warps (blockDim.y rows of step / 32 warps, at most kMaxGroup threads in all)
-        const int w = threadIdx.x >> 5, nw = step >> 5;
-        if ((threadIdx.x & 31) == 0) s_max[threadIdx.y * nw + w] = rm;
-        __syncthreads();
-        for (int i = 0; i < nw; ++i) rm = max(rm, s_max[threadIdx.y * nw + i]);
-    }
-    if (!active) return;  // rows do not share a warp
-    auto emit = [&](int u, const uint4& ua, const uint4& ub, uint32_t um) {
-        const int lane = threadIdx.x & 31;
-        uint2 codes;
-        uint32_t scale;
-        if constexpr (FMT == kMxfp4) um = max(um, __shfl_xor_sync(0xffffffffu, um, 1));  // a block is two units
-        quantize_unit<FMT>(ua, ub, um, rm, codes, scale);
-        if (u < units) *reinterpret_cast<uint2*>(p.codes + (size_t)row * (p.K / 2) + (size_t)u * 8) = codes;
-        // 4 scales of a tile row are one aligned word
-        constexpr int kPer = block_of(FMT) / kUnit;  // units per block
-        uint32_t word = u < units ? scale << (8 * ((lane / kPer) & 3)) : 0u;
-        word = (lane % kPer == 0) ? word : 0u;
-#pragma unroll
-        for (int off = 1; off < 4 * kPer; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
-        if (lane % (4 * kPer) == 0 && u < units)
-            *reinterpret_cast<uint32_t*>(p.scales + scale_offset(row, u / kPer, p.tiles)) = word;
     };
+    int buf = 0;
+    load(blockIdx.x);
+    for (int g = blockIdx.x; g < groups; g += gridDim.x, buf ^= 1) {
+        const int row = g * blockDim.y + threadIdx.y;
+        const bool active = row < p.rows;  // (rows do not share a warp)
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(active ? row : 0) * p.K);
+        uint4 ca[kHold], cb[kHold];
+        uint32_t bm[kHold], rm = 0;
 #pragma unroll
-    for (int h = 0; h < kHold; ++h)
-        if (static_cast<int>(threadIdx.x & ~31u) + h * step < units) emit(threadIdx.x + h * step, a[h], b[h], bm[h]);
-    for (int u0 = static_cast<int>(threadIdx.x & ~31u) + kHold * step; u0 < units; u0 += step) {
-        const int u = u0 + (threadIdx.x & 31);
-        uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-        if (u < units) {
-            ua = __ldg(src + 2 * u);
-            ub = __ldg(src + 2 * u + 1);
+        for (int h = 0; h < kHold; ++h) {
+            ca[h] = a[h];
+            cb[h] = b[h];
+            bm[h] = amax_bits16(ca[h], cb[h]);
+            rm = max(rm, bm[h]);
         }
-        emit(u, ua, ub, amax_bits16(ua, ub));
-    }
-    if (threadIdx.x == 0) {
-        float g = 1.0f;
-        if (FMT == kNvfp4)
-            g = pow2f(max(static_cast<int>(rm >> 7) - 127 - 11 + ((rm & 127u) > 40u ? 1 : 0), -100));
-        p.row_scale[row] = rm < 0x7f80u ? g : __uint_as_float(0x7fc00000u);
+        for (int u = threadIdx.x + kHold * step; u < units; u += step)
+            if (active) rm = max(rm, amax_bits16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1)));
+        if (g + gridDim.x < groups) load(g + gridDim.x);
+        rm = __reduce_max_sync(0xffffffffu, rm);
+        if (step > 32) {  // the row's warps (blockDim.y rows of step / 32 warps, at most kMaxGroup threads in all)
+            const int w = threadIdx.x >> 5, nw = step >> 5;
+            if (lane == 0) s_max[buf][threadIdx.y * nw + w] = rm;
+            __syncthreads();  // (two buffers: the next row's maxima do not overwrite those still being read)
+            rm = __reduce_max_sync(0xffffffffu, s_max[buf][threadIdx.y * nw + (lane < nw ? lane : 0)]);
+        }
+        if (!active) continue;
+        auto emit = [&](int u, const uint4& ua, const uint4& ub, uint32_t um) {
+            uint2 codes;
+            uint32_t scale;
+            if constexpr (FMT == kMxfp4) um = max(um, __shfl_xor_sync(0xffffffffu, um, 1));  // a block is two units
+            quantize_unit<FMT>(ua, ub, um, rm, codes, scale);
+            if (u < units) *reinterpret_cast<uint2*>(p.codes + (size_t)row * (p.K / 2) + (size_t)u * 8) = codes;
+            // 4 scales of a tile row are one aligned word
+            constexpr int kPer = block_of(FMT) / kUnit;  // units per block
+            uint32_t word = u < units ? scale << (8 * ((lane / kPer) & 3)) : 0u;
+            word = (lane % kPer == 0) ? word : 0u;
+#pragma unroll
+            for (int off = kPer; off < 4 * kPer; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
+            if (lane % (4 * kPer) == 0 && u < units)
+                *reinterpret_cast<uint32_t*>(p.scales + scale_offset(row, u / kPer, p.tiles)) = word;
+        };
+        const int u0 = static_cast<int>(threadIdx.x & ~31u);
+#pragma unroll
+        for (int h = 0; h < kHold; ++h)
+            if (u0 + h * step < units) emit(threadIdx.x + h * step, ca[h], cb[h], bm[h]);
+        for (int v0 = u0 + kHold * step; v0 < units; v0 += step) {
+            const int u = v0 + lane;
+            uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+            if (u < units) {
+                ua = __ldg(src + 2 * u);
+                ub = __ldg(src + 2 * u + 1);
+            }
+            emit(u, ua, ub, amax_bits16(ua, ub));
+        }
+        if (threadIdx.x == 0) {
+            float gs = 1.0f;
+            if (FMT == kNvfp4)
+                gs = pow2f(max(static_cast<int>(rm >> 7) - 127 - 11 + ((rm & 127u) > 40u ? 1 : 0), -100));
+            p.row_scale[row] = rm < 0x7f80u ? gs : __uint_as_float(0x7fc00000u);
+        }
     }
 }
 
-// 16 codes -> 16 bf16 values per thread (exact: see the header).  Bound: HBM.
+// 16 codes -> 16 bf16 values per thread and step (exact: see the header), rows and threads as above.
+// Bound: HBM.
 template <int FMT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(quant::kMaxGroup)
     gdn_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int rows, int K, int tiles,
                           uint16_t* out) {
     using namespace quant;
     const int units = K / kUnit;
-    const size_t total = (size_t)rows * units;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
-        const size_t row = i / units;
-        const int u = static_cast<int>(i - row * units);
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-        const uint32_t sb = __ldg(scales + scale_offset(row, FMT == kNvfp4 ? u : u >> 1, tiles));
-        float s;
-        if (FMT == kNvfp4) s = e4m3_value(sb);
-        else s = sb == 255u ? __uint_as_float(0x7fc00000u) : (sb == 0u ? __uint_as_float(1u << 22) : __uint_as_float(sb << 23));
-        s *= __ldg(row_scale + row);
-        uint32_t o[8];
+    for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < rows; row += (int64_t)gridDim.x * blockDim.y) {
+        const float g = __ldg(row_scale + row);
+        const uint2* src = reinterpret_cast<const uint2*>(codes + (size_t)row * (K / 2));
+        uint4* dst = reinterpret_cast<uint4*>(out + (size_t)row * K);
+        for (int u = threadIdx.x; u < units; u += blockDim.x) {
+            const uint2 c = __ldg(src + u);
+            const uint32_t sb = __ldg(scales + scale_offset(row, FMT == kNvfp4 ? u : u >> 1, tiles));
+            float s;
+            if (FMT == kNvfp4) s = e4m3_value(sb);
+            else s = sb == 255u ? __uint_as_float(0x7fc00000u) : (sb == 0u ? __uint_as_float(1u << 22) : __uint_as_float(sb << 23));
+            s *= g;
+            uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t byte = ((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xffu;
-            uint32_t h;
-            asm("{\n\t.reg .b8 b0, b1;\n\tmov.b16 {b0, b1}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}\n"
-                : "=r"(h)
-                : "h"(static_cast<uint16_t>(byte)));
-            const __half2 h2 = *reinterpret_cast<__half2*>(&h);
-            o[j] = pack_bf16x2(__low2float(h2) * s, __high2float(h2) * s);
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t byte = ((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xffu;
+                uint32_t h;
+                asm("{\n\t.reg .b8 b0, b1;\n\tmov.b16 {b0, b1}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}\n"
+                    : "=r"(h)
+                    : "h"(static_cast<uint16_t>(byte)));
+                const __half2 h2 = *reinterpret_cast<__half2*>(&h);
+                o[j] = pack_bf16x2(__low2float(h2) * s, __high2float(h2) * s);
+            }
+            dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        uint4* dst = reinterpret_cast<uint4*>(out + i * kUnit);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
