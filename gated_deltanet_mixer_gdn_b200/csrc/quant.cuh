@@ -64,13 +64,24 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffffu)));
 }
 
-// Largest bf16 magnitude of 16 packed elements, as bits (integer order: NaN > infinity > finite).
+// Largest bf16 magnitude of 16 packed elements, as bits (a NaN among them: 0x7fff, above infinity).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) {
     const uint32_t m = 0x7fff7fffu;
-    uint32_t r = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
-    r = __vmaxu2(r, __vmaxu2(__vmaxu2(b.x & m, b.y & m), __vmaxu2(b.z & m, b.w & m)));
+    uint32_t r = max_bf16x2(max_bf16x2(a.x & m, a.y & m), max_bf16x2(a.z & m, a.w & m));
+    r = max_bf16x2(r, max_bf16x2(max_bf16x2(b.x & m, b.y & m), max_bf16x2(b.z & m, b.w & m)));
     return max(r & 0xffffu, r >> 16);
 }
+
+// v rounded to 16 significant bits.  A quotient formed with a rounded reciprocal may miss an exact tie by a
+// relative 2^-22; the quotients taken here (8 bits over at most 4) are ties of the format rounded to next
+// or at least a relative 1/255 away from one, so this restores the former and keeps the latter apart (and
+// keeps the sign of a zero).
+__device__ __forceinline__ float snap16(float v) { return __uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u); }
 
 // The 16 codes of one thread's unit and its block's scale byte, from the unit, the block's and the
 // row's largest magnitudes.
@@ -83,11 +94,11 @@ __device__ __forceinline__ void quantize_unit(const uint4& a, const uint4& b, ui
         // amax = (1 + m / 128) 2^e against 2688 = (1 + 40 / 128) 2^11
         const int j = max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100);
         const float inv_g = pow2f(-j);
-        // the quotient of an 8-bit number by 6 is never within 2^-24 of a midpoint of E4M3 unless it
-        // is one, so rounding it to f32 first changes nothing
-        scale = e4m3_bits(__fdiv_rn(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g, 6.0f));
+        scale = e4m3_bits(snap16(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g * (1.0f / 6.0f)));
         const float s = e4m3_value(scale);
-        inv = s > 0.0f ? __frcp_rn(s) * inv_g : 0.0f;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        inv = s > 0.0f ? r * inv_g : 0.0f;
     } else {
         const int e = max(static_cast<int>(block_max >> 7) - 127 - 2, -127);
         scale = static_cast<uint32_t>(e + 127);
@@ -106,10 +117,8 @@ __device__ __forceinline__ void quantize_unit(const uint4& a, const uint4& b, ui
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
     }
     if constexpr (FMT == kNvfp4) {
-        // the reciprocal is rounded, so an exact tie may be off by 2^-23: rounding to 16 significant
-        // bits restores it (x / s is a tie or at least 2^-9 away from one) and keeps the sign of a zero
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float((__float_as_uint(v[i]) + 0x80u) & 0xffffff00u);
+        for (int i = 0; i < 16; ++i) v[i] = snap16(v[i]);
     }
     codes.x = pack_e2m1x8(v);
     codes.y = pack_e2m1x8(v + 8);
