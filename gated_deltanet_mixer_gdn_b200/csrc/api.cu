@@ -1340,6 +1340,22 @@ bool make_scale_map(CUtensorMap* m, const uint8_t* base, int64_t tiles, uint32_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launch of a projection behind its quantisation (the previous launch on the stream): its prologue may run
+// before the quantisation ends.  attr[0] is filled in; n attributes in all.
+cudaLaunchConfig_t after_quantize(dim3 grid, int threads, uint32_t smem, cudaStream_t stream, cudaLaunchAttribute* attr,
+                                  int n) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cfg;
+}
+
 template <int FMT>
 int qproj_pairs(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
     CUtensorMap mW, mX, mSw, mSx;
@@ -1354,32 +1370,44 @@ int qproj_pairs(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, in
     const int64_t ntiles = (int64_t)((p.T + qproj::duo::kTileM - 1) / qproj::duo::kTileM) *
                            ((p.N + qproj::duo::kTileN - 1) / qproj::duo::kTileN);
     const int pairs = (int)(ntiles < nsm / 2 ? ntiles : nsm / 2);
-    kernel<<<2 * pairs, qproj::duo::kDuoThreads, qproj::duo::SMEM_BYTES, stream>>>(mW, mX, mSw, mSx, p);
-    return cuda_status(cudaGetLastError());
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = after_quantize(dim3(2 * pairs), qproj::duo::kDuoThreads, qproj::duo::SMEM_BYTES, stream, attr, 1);
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, mSw, mSx, p));
 }
 
 template <int FMT, int BN>
-int qproj_tiles(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
+int qproj_few(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
+    using C = qproj::few::Cfg<BN>;
     CUtensorMap mW, mX;
-    if (!make_code_map(&mW, cw, p.K, p.N, qproj::BM) || !make_code_map(&mX, cx, p.K, p.T, BN)) return GDN_ERR_CUDA;
-    using C = qproj::Cfg<BN>;
-    auto kernel = gdn_qproj_kernel<FMT, BN>;
-    int st = smem_optin(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES);
+    if (!make_code_map(&mW, cw, p.K, p.N, qproj::few::kTileN) || !make_code_map(&mX, cx, p.K, p.T, BN)) return GDN_ERR_CUDA;
+    auto kernel = gdn_qproj_few_kernel<FMT, BN>;
+    const int st = smem_optin(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES);
     if (st != GDN_OK) return st;
-    const dim3 grid((p.N + qproj::BM - 1) / qproj::BM, (p.T + BN - 1) / BN);
-    kernel<<<grid, qproj::kThreads, C::SMEM_BYTES, stream>>>(mW, mX, p);
-    return cuda_status(cudaGetLastError());
+    // clusters that share a tile's K while the tiles leave SMs idle, at least two stages each
+    const int tiles = (p.N + qproj::few::kTileN - 1) / qproj::few::kTileN, steps = (p.K + qproj::BK - 1) / qproj::BK;
+    int split = nsm / tiles;
+    if (split > steps / 2) split = steps / 2;
+    if (split > qproj::few::kMaxSplit) split = qproj::few::kMaxSplit;
+    if (split < 1) split = 1;
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = split;
+    const cudaLaunchConfig_t cfg = after_quantize(dim3(tiles, 1, split), qproj::few::kThreads, C::SMEM_BYTES, stream, attr, split > 1 ? 2 : 1);
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, p));
 }
 
 template <int FMT>
 int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
-    if (p.T <= 16) return qproj_tiles<FMT, 16>(cx, cw, p, stream);
-    if (p.T <= 64) return qproj_tiles<FMT, 64>(cx, cw, p, stream);
-    if (p.T <= 128) return qproj_tiles<FMT, 128>(cx, cw, p, stream);
     int dev = 0, nsm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return GDN_ERR_CUDA;
+    if (p.T <= 16) return qproj_few<FMT, 16>(cx, cw, p, nsm, stream);
+    if (p.T <= 32) return qproj_few<FMT, 32>(cx, cw, p, nsm, stream);
+    if (p.T <= 64) return qproj_few<FMT, 64>(cx, cw, p, nsm, stream);
+    if (p.T <= 128) return qproj_few<FMT, 128>(cx, cw, p, nsm, stream);
     return qproj_pairs<FMT>(cx, cw, p, nsm, stream);
 }
 

@@ -93,47 +93,64 @@ __device__ __forceinline__ uint16_t* output_at(const Params& p, int n, int t) {
     return g.dst + (size_t)t * g.ld + (n - g.col0);
 }
 
-constexpr int BM = 128;                              // features per tile (rows of the A operand)
-constexpr uint32_t W_BYTES = BM * BK / 2;            // 16 KB
-constexpr uint32_t S_BYTES = 4 * quant::kTileBytes;  // scales of 128 rows, at most
-constexpr int kThreads = 192;                        // warp 0 loads, warp 1 products, warps 2-5 epilogue
+constexpr uint32_t S_BYTES = 4 * quant::kTileBytes;  // scales of 128 rows and a stage, at most
+
+// The projections are launched while the call's quantisation still runs (programmatic launch); before anything
+// it wrote is read they wait for its end.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------- few tokens: the weights' rows as lanes
+namespace few {
+constexpr int kTileN = 128;                           // features per tile (rows of the A operand)
+constexpr uint32_t W_BYTES = kTileN * BK / 2;         // 16 KB
+constexpr int kThreads = 192;                         // warp 0 loads, warp 1 products, warps 2-5 epilogue
+constexpr int kMaxSplit = 8;                          // CTAs of a cluster that share a tile's K
 
 template <int BN>
 struct Cfg {
     static constexpr uint32_t X_BYTES = BN * BK / 2;
     static constexpr uint32_t STAGE_BYTES = W_BYTES + X_BYTES + 2 * S_BYTES;
-    static constexpr int kStages = 6;
+    static constexpr int kStages = BN <= 32 ? 9 : BN <= 64 ? 7 : 6;
     static constexpr uint32_t OFF_MISC = kStages * STAGE_BYTES;
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 256 + 1024;
-    // tensor memory: the sums (BN columns), then per stage 16 columns of weight scales and 16 of token scales
+    // tensor memory: the sums (BN columns), then per stage 16 columns of weight scales and 16 of token
+    // scales; a stage's columns are free when its shared memory is
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(BN + 32 * kStages <= 512, "tensor memory");
     static_assert(X_BYTES % 1024 == 0, "swizzle atoms");
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(OFF_MISC >= BN * kTileN * 4, "the partial sums reuse the ring");
 };
-
+}  // namespace few
 }  // namespace qproj
 
-// One CTA per 128 features x BN tokens: the weights are the A operand (128 rows), the tokens the B
-// operand, so that few tokens still fill the tensor core's 128 lanes.  Token tiles start at multiples
-// of 128 rows (BN = 128), or there is one (BN < 128), so that their scales are whole tiles.
+// At most 128 tokens: a tile is 128 features x all BN (>= T) tokens, the weights the A operand, so that few
+// tokens still fill the tensor core's 128 lanes.  Bound: reading the weights once.  Where the tiles are fewer
+// than the SMs a cluster of gridDim.z CTAs shares one tile's K; each leaves its sums in shared memory and adds
+// the others' for its part of the tokens, in rank order.  The loads of the first stages' weights, and all of
+// the prologue, run before the quantisation of the tokens (the previous launch of the call) is waited for.
 template <int FMT, int BN>
-__global__ void __launch_bounds__(qproj::kThreads, 1)
-    gdn_qproj_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                     const qproj::Params p) {
+__global__ void __launch_bounds__(qproj::few::kThreads, 1)
+    gdn_qproj_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                         const qproj::Params p) {
     using namespace qproj;
+    using namespace qproj::few;
     using C = Cfg<BN>;
     constexpr int kTiles = kTilesPerStage(FMT);
-    constexpr uint32_t ID = idesc(FMT, BM, BN);
+    constexpr uint32_t ID = idesc(FMT, kTileN, BN);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
     uint64_t* empty = full + C::kStages;
     uint64_t* done = empty + C::kStages;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 128);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 192);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n0 = blockIdx.x * BM, t0 = blockIdx.y * BN;
-    const int ksteps = (p.K + BK - 1) / BK;
+    const int n0 = blockIdx.x * kTileN;
+    const int split = gridDim.z, rank = blockIdx.z;  // (the cluster spans z)
+    const int all = (p.K + BK - 1) / BK;
+    const int k0 = static_cast<int>(static_cast<int64_t>(all) * rank / split);
+    const int ksteps = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / split) - k0;
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(qproj::kThreads, 1)
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
-    if (warp == 0) {
+    if (warp == 1) {
         tmem_alloc(s_tmem, C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -162,77 +179,137 @@ __global__ void __launch_bounds__(qproj::kThreads, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int issued = 0;
-            for (int ks = 0; ks < ksteps; ++ks) {
-                const int s = ks % C::kStages;
-                if (ks >= C::kStages) wait1(&empty[s], ((ks / C::kStages) - 1) & 1, kErrTimeoutTma);
-                if (broken) break;  // nothing more is requested
-                uint8_t* st = smem + s * C::STAGE_BYTES;
-                const uint32_t sbytes = min(kTiles, p.tiles - ks * kTiles) * quant::kTileBytes;
-                mbar_arrive_expect_tx(&full[s], W_BYTES + C::X_BYTES + 2 * sbytes);
-                tma_load_2d(st, &tmW, ks * (BK / 2), n0, &full[s]);
-                tma_load_2d(st + W_BYTES, &tmX, ks * (BK / 2), t0, &full[s]);
-                bulk_load(st + W_BYTES + C::X_BYTES,
-                          p.sw + ((size_t)(n0 >> 7) * p.tiles + ks * kTiles) * quant::kTileBytes, sbytes, &full[s]);
-                bulk_load(st + W_BYTES + C::X_BYTES + S_BYTES,
-                          p.sx + ((size_t)(t0 >> 7) * p.tiles + ks * kTiles) * quant::kTileBytes, sbytes, &full[s]);
-                issued = ks + 1;
-            }
-            // no copy is in flight when the CTA exits, whatever the other warps did
-            for (int ks = max(issued - C::kStages, 0); ks < issued; ++ks)
-                mbar_wait(&full[ks % C::kStages], (ks / C::kStages) & 1);
-        }
+        // ---------------- loads; a stage's bytes: codes of 128 features and BN tokens, their scale tiles
+        auto scale_bytes = [&](int ks) { return min(kTiles, p.tiles - (k0 + ks) * kTiles) * quant::kTileBytes; };
+        auto load_w = [&](int ks, int s) {
+            uint8_t* st = smem + s * C::STAGE_BYTES;
+            mbar_arrive_expect_tx(&full[s], W_BYTES + C::X_BYTES + 2 * scale_bytes(ks));
+            tma_load_2d(st, &tmW, (k0 + ks) * (BK / 2), n0, &full[s]);
+            bulk_load(st + W_BYTES + C::X_BYTES,
+                      p.sw + ((size_t)blockIdx.x * p.tiles + (k0 + ks) * kTiles) * quant::kTileBytes, scale_bytes(ks), &full[s]);
+        };
+        auto load_x = [&](int ks, int s) {
+            uint8_t* st = smem + s * C::STAGE_BYTES;
+            tma_load_2d(st + W_BYTES, &tmX, (k0 + ks) * (BK / 2), 0, &full[s]);
+            bulk_load(st + W_BYTES + C::X_BYTES + S_BYTES, p.sx + (size_t)(k0 + ks) * kTiles * quant::kTileBytes,
+                      scale_bytes(ks), &full[s]);
+        };
+        const int head = min(C::kStages, ksteps);
+        if (elect_one())
+            for (int ks = 0; ks < head; ++ks) load_w(ks, ks);
         __syncwarp();
+        grid_wait();
+        if (elect_one())
+            for (int ks = 0; ks < head; ++ks) load_x(ks, ks);
+        __syncwarp();
+        int issued = head;
+        uint32_t s = 0, ph = 0;
+        for (; issued < ksteps; ++issued) {
+            wait1(&empty[s], ph, kErrTimeoutTma);
+            if (broken) break;
+            if (elect_one()) {
+                load_w(issued, s);
+                load_x(issued, s);
+            }
+            __syncwarp();
+            if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+        // no copy is in flight when the CTA exits, whatever the other warps did
+        for (int ks = max(issued - C::kStages, 0); ks < issued; ++ks)
+            mbar_wait(&full[ks % C::kStages], (ks / C::kStages) & 1);
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int ks = 0; ks < ksteps; ++ks) {
-                const int s = ks % C::kStages;
-                wait1(&full[s], (ks / C::kStages) & 1, kErrTimeoutTma);
-                if (broken) break;
-                tc_fence_after();
-                const uint32_t aW = sbase + s * C::STAGE_BYTES, aX = aW + W_BYTES, aSw = aX + C::X_BYTES;
-                const uint32_t cS = tbase + BN + 32 * s;
-                const int tiles = min(kTiles, p.tiles - ks * kTiles);
-                for (int i = 0; i < tiles; ++i) {
-                    copy_scales(cS + 4 * i, scale_desc(aSw + i * quant::kTileBytes));
-                    copy_scales(cS + 16 + 4 * i, scale_desc(aSw + S_BYTES + i * quant::kTileBytes));
+        const uint64_t kDesc = sw128_desc(0, 16, 1024), sDesc = scale_desc(0);
+        uint32_t s = 0, ph = 0;
+        for (int ks = 0; ks < ksteps; ++ks) {
+            wait1(&full[s], ph, kErrTimeoutTma);
+            if (broken) break;
+            tc_fence_after();
+            const uint32_t aW = sbase + s * C::STAGE_BYTES;
+            const uint64_t dW = desc_at(kDesc, aW), dX = desc_at(kDesc, aW + W_BYTES);
+            const uint64_t dS = desc_at(sDesc, aW + W_BYTES + C::X_BYTES);
+            const uint32_t cW = tbase + BN + 32 * s, cX = cW + 16;
+            const int nk = min(BK / kMmaK, (p.K - (k0 + ks) * BK) / kMmaK);
+            const uint32_t more = ks > 0;
+            if (elect_one()) {
+                // (at the end of K some tiles hold an earlier stage's scales: no product reads them)
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    copy_scales(cW + 4 * i, dS + 32 * i);
+                    copy_scales(cX + 4 * i, dS + (S_BYTES >> 4) + 32 * i);
                 }
-                const int nk = min(BK / kMmaK, (p.K - ks * BK) / kMmaK);
-                for (int kk = 0; kk < nk; ++kk) {
-                    const int tile = FMT == quant::kNvfp4 ? kk : kk >> 1;
-                    const uint32_t id = FMT == quant::kNvfp4 ? ID : ID | scale_id(2 * (kk & 1));
-                    mma_scaled<FMT>(tbase, sw128_desc(aW + kk * 32, 16, 1024), sw128_desc(aX + kk * 32, 16, 1024), id,
-                                    cS + 4 * tile, cS + 16 + 4 * tile, (ks > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < BK / kMmaK; ++kk) {
+                    constexpr bool nv = FMT == quant::kNvfp4;
+                    const int tile = nv ? kk : kk >> 1;
+                    if (kk < nk)
+                        mma_scaled<FMT>(tbase, dW + 2 * kk, dX + 2 * kk, nv ? ID : ID | scale_id(2 * (kk & 1)), cW + 4 * tile,
+                                        cX + 4 * tile, kk > 0 ? 1u : more);
                 }
                 mma_commit(&empty[s]);
+                if (ks + 1 == ksteps) mma_commit(done);
             }
-            mma_commit(done);
+            __syncwarp();
+            if (++s == C::kStages) s = 0, ph ^= 1;
         }
-        __syncwarp();
     } else {
+        // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
-        const uint32_t tl = static_cast<uint32_t>(32 * q4) << 16;
-        const int n = n0 + 32 * q4 + lane;
-        const float gw = n < p.N ? __ldg(p.gw + n) : 0.0f;
+        float* part = reinterpret_cast<float*>(smem);
         wait1(done, 0, kErrTimeoutMma);
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < BN / 16; ++j) {
             float v[16];
-            tmem_ld16(tbase + tl + 16 * j, v);
+            tmem_ld16(tbase + (static_cast<uint32_t>(32 * q4) << 16) + 16 * j, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int t = t0 + 16 * j + e;
-                if (n < p.N && t < p.T) *output_at(p, n, t) = float_to_bf16_bits(v[e] * (gw * __ldg(p.gx + t)));
-            }
+            for (int e = 0; e < 16; ++e) part[(16 * j + e) * kTileN + 32 * q4 + lane] = v[e];
         }
     }
     tc_fence_before();
-    __syncthreads();
-    if (warp == 0) tmem_dealloc(tbase, C::TMEM_COLS);
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    if (warp >= 2) {
+        // ---------------- this rank's tokens: four features per lane, a token's 128 per warp
+        grid_wait();  // the tokens' row scales
+        const int n = n0 + 4 * lane;
+        float gw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? __ldg(p.gw + n + e) : 0.0f;
+        int end;
+        const GemmSegment g = segment_of(p, n, end);
+        const bool whole = n + 4 <= end && (((n - g.col0) | g.ld) & 3) == 0;  // (segments start on 16 bytes)
+        const uint32_t mine = sbase + 16 * lane;
+        for (int t = rank + split * (warp - 2); t < p.T; t += 4 * split) {
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int r = 0; r < split; ++r) {
+                float4 b;
+                uint32_t at = mine + t * kTileN * 4;
+                if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(r));
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                             : "r"(at)
+                             : "memory");
+                a.x += b.x;
+                a.y += b.y;
+                a.z += b.z;
+                a.w += b.w;
+            }
+            const float gx = __ldg(p.gx + t);
+            const uint32_t lo = pack_bf16x2(a.x * (gx * gw[0]), a.y * (gx * gw[1]));
+            const uint32_t hi = pack_bf16x2(a.z * (gx * gw[2]), a.w * (gx * gw[3]));
+            if (whole) {
+                *reinterpret_cast<uint2*>(g.dst + (size_t)t * g.ld + (n - g.col0)) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < p.N) *output_at(p, n + e, t) = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+            }
+        }
+    }
+    if (split > 1) cluster_sync();  // the other CTAs have read this one's sums
+    if (warp == 1) tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
 // ---------------------------------------------------------------- many tokens: pairs of SMs
@@ -416,6 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
 
     if (warp == 0) {
         // ---------------- loads: this CTA's rows; the bytes of both CTAs complete on rank 0's barrier
+        grid_wait();
         uint32_t q = 0;
         for (int t = first; t < ntiles && !broken; t += step) {
             int tm, tn;
@@ -504,6 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
         const int q4 = warp & 3, et = tid - 64;
         const uint32_t tl = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t free_bar = cluster_addr(acc_free, 0);
+        grid_wait();
         uint32_t it = 0;
         for (int t = first; t < ntiles; t += step, ++it) {
             int tm, tn;

@@ -144,6 +144,9 @@ template <int FMT, int kHold>
 __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const quant::Params p) {
     using namespace quant;
     __shared__ uint32_t s_max[2][kMaxGroup / 32];
+    // a projection launched behind this kernel may start its prologue (it waits for this grid's end before
+    // it reads what is written here)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int units = p.K / kUnit, step = blockDim.x, lane = threadIdx.x & 31;
     const int groups = (p.rows + blockDim.y - 1) / blockDim.y;  // steps of all CTAs
     uint4 a[kHold], b[kHold];
