@@ -13,8 +13,10 @@ There is no CPU path: if the library is missing the calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 from typing import Dict, Optional, Sequence
@@ -182,6 +184,22 @@ def _device_of(qkv: torch.Tensor) -> torch.device:
     if not qkv.is_cuda:
         raise GdnError("the mixer runs on the GPU only: pass CUDA tensors")
     return qkv.device
+
+
+_dims_of = functools.lru_cache(maxsize=64)(_dims_c)  # (the struct is only read)
+
+
+# the current stream of a device by its index (3 us of the small calls went into torch.cuda.current_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(device: torch.device, fn, *args) -> int:
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _raw_stream(device.index))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(device.index))
 
 
 def prefill(qkv, z, a, b, weights, init_state=None, init_conv=None, *, out=None, final_state=None,
@@ -473,93 +491,102 @@ def out_proj(y, w_out, *, dims: Dims = MODEL, out=None):
 
 
 QUANT_FORMATS = {"nvfp4": 0, "mxfp4": 1}
+_QUANT_BLOCK = {"nvfp4": 16, "mxfp4": 32}
+
+
+def _scale_shape(format: str, rows: int, K: int):
+    """Scales of [rows, K]: tiles of 128 rows x 4 blocks, 512 bytes each (gdn_quant_scale_bytes in all)."""
+    return (rows + 127) // 128, -(-K // (4 * _QUANT_BLOCK[format])), 512
 
 
 @dataclasses.dataclass(frozen=True)
 class QuantTensor:
     """Rows held in microscaled 4 bits (layouts in ``include/gdn.h``): what ``quantize`` returns and
     the 4-bit projections take as weights.  codes uint8 [rows, K/2]; scales uint8 [row blocks of 128,
-    tiles, 512]; row_scale f32 [rows]."""
+    tiles, 512]; row_scale f32 [rows]; all contiguous, on one device."""
 
     codes: torch.Tensor
     scales: torch.Tensor
     row_scale: torch.Tensor
     format: str
 
+    def __post_init__(self):
+        if self.format not in QUANT_FORMATS:
+            raise ValueError(f"format must be one of {sorted(QUANT_FORMATS)}, got {self.format!r}")
+        dev = getattr(self.codes, "device", None)
+        _need(self.codes, torch.uint8, "codes", dev)
+        _need(self.scales, torch.uint8, "scales", dev)
+        _need(self.row_scale, torch.float32, "row_scale", dev)
+        if self.codes.dim() != 2 or self.codes.shape[1] == 0 or self.codes.shape[1] % 32:
+            raise ValueError("codes must be [rows, K/2], K a multiple of 64")
+        rows, K = self.shape
+        if tuple(self.row_scale.shape) != (rows,) or tuple(self.scales.shape) != _scale_shape(self.format, rows, K):
+            raise ValueError("codes, scales and row_scale do not belong together")
+
     @property
     def shape(self):
-        return int(self.codes.shape[0]), 2 * int(self.codes.shape[1])
-
-
-def _quant_format(format: str) -> int:
-    if format not in QUANT_FORMATS:
-        raise ValueError(f"format must be one of {sorted(QUANT_FORMATS)}, got {format!r}")
-    return QUANT_FORMATS[format]
+        rows, half = self.codes.shape
+        return rows, 2 * half
 
 
 def _quant_checked(q: QuantTensor, name: str, device: torch.device):
+    """(format, rows, K, pointers); the tensor checked itself when it was made."""
     if not isinstance(q, QuantTensor):
         raise TypeError(f"{name} must be a QuantTensor")
-    rows, K = q.shape
-    _need(q.codes, torch.uint8, f"{name}.codes", device)
-    _need(q.scales, torch.uint8, f"{name}.scales", device)
-    _need(q.row_scale, torch.float32, f"{name}.row_scale", device)
-    if q.codes.dim() != 2 or q.row_scale.numel() != rows or \
-            q.scales.numel() != load_library().gdn_quant_scale_bytes(_quant_format(q.format), rows, K):
-        raise ValueError(f"{name}: codes, scales and row_scale do not belong together")
-    return _quant_format(q.format), rows, K
+    if q.codes.device != device:
+        raise ValueError(f"{name} must be on {device}, got {q.codes.device}")
+    rows, half = q.codes.shape
+    return QUANT_FORMATS[q.format], rows, 2 * half, (q.codes.data_ptr(), q.scales.data_ptr(), q.row_scale.data_ptr())
 
 
 def quantize(x, format: str = "nvfp4", *, out: Optional[QuantTensor] = None) -> QuantTensor:
     """x bf16 [rows, K] (K a multiple of 64) as microscaled 4-bit rows: "nvfp4" (blocks of 16 with E4M3
     scales and a power of two per row) or "mxfp4" (blocks of 32 with power-of-two scales)."""
     dev = _device_of(x)
-    fmt = _quant_format(format)
-    L = load_library()
+    if format not in QUANT_FORMATS:
+        raise ValueError(f"format must be one of {sorted(QUANT_FORMATS)}, got {format!r}")
     _need(x, torch.bfloat16, "x", dev)
     if x.dim() != 2:
         raise ValueError("quantize: x must be [rows, K]")
-    rows, K = int(x.shape[0]), int(x.shape[1])
+    rows, K = x.shape
     if K == 0 or K % 64:
         raise ValueError("quantize: K must be a multiple of 64")
     if out is None:
-        tile_blocks = L.gdn_quant_scale_bytes(fmt, 128, K) // 512
-        out = QuantTensor(torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
-                          torch.empty(((rows + 127) // 128, tile_blocks, 512), dtype=torch.uint8, device=dev),
-                          torch.empty((rows,), dtype=torch.float32, device=dev), format)
-    elif _quant_checked(out, "out", dev) != (fmt, rows, K):
+        out = object.__new__(QuantTensor)  # (made here: nothing to check)
+        out.__dict__.update(codes=x.new_empty((rows, K // 2), dtype=torch.uint8),
+                            scales=x.new_empty(_scale_shape(format, rows, K), dtype=torch.uint8),
+                            row_scale=x.new_empty((rows,), dtype=torch.float32), format=format)
+    fmt, orows, oK, ptrs = _quant_checked(out, "out", dev)
+    if out.format != format or (orows, oK) != (rows, K):
         raise ValueError("quantize: out has another format or shape")
-    with torch.cuda.device(dev):
-        st = L.gdn_quantize(fmt, rows, K, _ptr(x), _ptr(out.codes), _ptr(out.scales), _ptr(out.row_scale), _stream(dev))
-    _check(st, "gdn_quantize")
+    _check(_on(dev, load_library().gdn_quantize, fmt, rows, K, x.data_ptr(), *ptrs), "gdn_quantize")
     return out
 
 
 def dequantize(q: QuantTensor, *, out=None):
     """The values that 4-bit rows stand for, bf16 [rows, K] (exact)."""
+    if not isinstance(q, QuantTensor):
+        raise TypeError("q must be a QuantTensor")
     dev = _device_of(q.codes)
-    fmt, rows, K = _quant_checked(q, "q", dev)
+    fmt, rows, K, ptrs = _quant_checked(q, "q", dev)
     if out is None:
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=dev)
+        out = q.codes.new_empty((rows, K), dtype=torch.bfloat16)
     else:
         _need(out, torch.bfloat16, "out", dev)
         if tuple(out.shape) != (rows, K):
             raise ValueError("dequantize: out shape")
-    with torch.cuda.device(dev):
-        st = load_library().gdn_dequantize(fmt, rows, K, _ptr(q.codes), _ptr(q.scales), _ptr(q.row_scale), _ptr(out),
-                                           _stream(dev))
-    _check(st, "gdn_dequantize")
+    _check(_on(dev, load_library().gdn_dequantize, fmt, rows, K, *ptrs, out.data_ptr()), "gdn_dequantize")
     return out
 
 
-def _proj_out(out, widths, T: int, dev: torch.device, what: str):
+def _proj_out(out, x, T: int, widths, what: str):
     if out is None:
-        return [torch.empty((T, w), dtype=torch.bfloat16, device=dev) for w in widths]
+        return [x.new_empty((T, w)) for w in widths]
     for t, w in zip(out, widths):
-        _need(t, torch.bfloat16, f"{what} out", dev)
+        _need(t, torch.bfloat16, f"{what} out", x.device)
         if tuple(t.shape) != (T, w):
             raise ValueError(f"{what}: out shape")
-    return list(out)
+    return out
 
 
 def in_proj_quant(x, w_in: QuantTensor, *, dims: Dims = MODEL, out=None):
@@ -568,21 +595,17 @@ def in_proj_quant(x, w_in: QuantTensor, *, dims: Dims = MODEL, out=None):
     Returns (qkv [T,C], z [T,Vh*D], a [T,Vh], b [T,Vh]) bf16."""
     dev = _device_of(x)
     _need(x, torch.bfloat16, "x", dev)
-    fmt, N, K = _quant_checked(w_in, "w_in", dev)
+    fmt, N, K, ptrs = _quant_checked(w_in, "w_in", dev)
     C, VD, Vh = dims.conv_channels, dims.value_width, dims.num_v_heads
-    if x.dim() != 2 or int(x.shape[1]) != K or N != C + VD + 2 * Vh:
+    if x.dim() != 2 or x.shape[1] != K or N != C + VD + 2 * Vh:
         raise ValueError("in_proj_quant: shape mismatch")
-    T = int(x.shape[0])
+    T = x.shape[0]
     L = load_library()
-    qkv, z, a, b = _proj_out(out, (C, VD, Vh, Vh), T, dev, "in_proj_quant")
+    qkv, z, a, b = _proj_out(out, x, T, (C, VD, Vh, Vh), "in_proj_quant")
     ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
-    ws = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
-    dc = _dims_c(dims)
-    with torch.cuda.device(dev):
-        st = L.gdn_in_proj_quant(ctypes.byref(dc), fmt, T, K, _ptr(x), _ptr(w_in.codes), _ptr(w_in.scales),
-                                 _ptr(w_in.row_scale), _ptr(qkv), _ptr(z), _ptr(b), _ptr(a), _ptr(ws), ws_bytes,
-                                 _stream(dev))
-    _check(st, "gdn_in_proj_quant")
+    ws = x.new_empty((ws_bytes,), dtype=torch.uint8)
+    _check(_on(dev, L.gdn_in_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, K, x.data_ptr(), *ptrs, qkv.data_ptr(),
+               z.data_ptr(), b.data_ptr(), a.data_ptr(), ws.data_ptr(), ws_bytes), "gdn_in_proj_quant")
     return qkv, z, a, b
 
 
@@ -591,19 +614,16 @@ def out_proj_quant(y, w_out: QuantTensor, *, dims: Dims = MODEL, out=None):
     [T, hidden]."""
     dev = _device_of(y)
     _need(y, torch.bfloat16, "y", dev)
-    fmt, hidden, K = _quant_checked(w_out, "w_out", dev)
-    if y.dim() != 2 or K != dims.value_width or int(y.shape[1]) != K:
+    fmt, hidden, K, ptrs = _quant_checked(w_out, "w_out", dev)
+    if y.dim() != 2 or K != dims.value_width or y.shape[1] != K:
         raise ValueError("out_proj_quant: shape mismatch")
-    T = int(y.shape[0])
+    T = y.shape[0]
     L = load_library()
-    out, = _proj_out(None if out is None else [out], (hidden,), T, dev, "out_proj_quant")
+    out, = _proj_out(None if out is None else [out], y, T, (hidden,), "out_proj_quant")
     ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
-    ws = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
-    dc = _dims_c(dims)
-    with torch.cuda.device(dev):
-        st = L.gdn_out_proj_quant(ctypes.byref(dc), fmt, T, hidden, _ptr(y), _ptr(w_out.codes), _ptr(w_out.scales),
-                                  _ptr(w_out.row_scale), _ptr(out), _ptr(ws), ws_bytes, _stream(dev))
-    _check(st, "gdn_out_proj_quant")
+    ws = y.new_empty((ws_bytes,), dtype=torch.uint8)
+    _check(_on(dev, L.gdn_out_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, hidden, y.data_ptr(), *ptrs,
+               out.data_ptr(), ws.data_ptr(), ws_bytes), "gdn_out_proj_quant")
     return out
 
 
@@ -676,21 +696,25 @@ def _pool_checked(state_pool, conv_pool, dims: Dims, what: str):
     dev = _device_of(state_pool)
     _need(state_pool, torch.float32, "state_pool", dev)
     _need(conv_pool, torch.float32, "conv_pool", dev)
-    P = int(state_pool.shape[0])
-    if tuple(state_pool.shape) != (P, dims.num_v_heads, dims.head_dim, dims.head_dim) or \
-            tuple(conv_pool.shape) != (P, dims.conv_width - 1, dims.conv_channels):
+    P, D = state_pool.shape[0], dims.head_dim
+    if state_pool.shape != (P, dims.num_v_heads, D, D) or \
+            conv_pool.shape != (P, dims.conv_width - 1, dims.conv_channels):
         raise ValueError(f"{what}: pool shapes")
     return dev, P
 
 
-def _host_table(rows) -> torch.Tensor:
-    t = rows.detach() if isinstance(rows, torch.Tensor) else torch.tensor(list(rows), dtype=torch.int64)
-    if t.dim() != 1 or t.dtype not in (torch.int32, torch.int64):
-        raise TypeError("pool rows must be a list or a one-dimensional int32 / int64 tensor")
-    t = t.to("cpu", torch.int64)
-    if t.numel() and (int(t.min()) < -(1 << 31) or int(t.max()) >= 1 << 31):
-        raise ValueError("pool rows out of range")
-    return t.to(torch.int32).contiguous()
+def _host_table(rows):
+    """(int32 array, count) of pool rows: from a list of integers, or a one-dimensional int32 / int64
+    tensor (one on the GPU is copied to the host)."""
+    if isinstance(rows, torch.Tensor):
+        if rows.dim() != 1 or rows.dtype not in (torch.int32, torch.int64):
+            raise TypeError("pool rows must be a list or a one-dimensional int32 / int64 tensor")
+        rows = rows.tolist()
+    rows = list(rows)
+    try:
+        return array.array("i", rows), len(rows)
+    except OverflowError:
+        raise ValueError("pool rows out of range") from None
 
 
 def copy_slots(src, dst, state_pool, conv_pool, *, dims: Dims = MODEL):
@@ -698,21 +722,17 @@ def copy_slots(src, dst, state_pool, conv_pool, *, dims: Dims = MODEL):
     pairs at once and in place: forks (one source, several destinations), reorderings, swaps and
     cycles.  src, dst: lists or int32 / int64 tensors (host ones do not synchronise), no dst twice."""
     dev, P = _pool_checked(state_pool, conv_pool, dims, "copy_slots")
-    s, d = _host_table(src), _host_table(dst)
-    if s.numel() != d.numel():
+    (s, n), (d, m) = _host_table(src), _host_table(dst)
+    if n != m:
         raise ValueError("copy_slots: one source per destination")
-    dc = _dims_c(dims)
-    with torch.cuda.device(dev):
-        st = load_library().gdn_copy_slots(ctypes.byref(dc), int(d.numel()), ctypes.c_void_p(s.data_ptr()),
-                                           ctypes.c_void_p(d.data_ptr()), P, _ptr(state_pool), _ptr(conv_pool),
-                                           _stream(dev))
-    _check(st, "gdn_copy_slots")
+    _check(_on(dev, load_library().gdn_copy_slots, ctypes.byref(_dims_of(dims)), n, s.buffer_info()[0],
+               d.buffer_info()[0], P, state_pool.data_ptr(), conv_pool.data_ptr()), "gdn_copy_slots")
 
 
 def free_slots(slots, state_pool, conv_pool, *, dims: Dims = MODEL):
     """Clears pool rows (zero state and history: a new sequence starts from them)."""
-    d = _host_table(slots)
-    copy_slots(torch.full_like(d, -1), d, state_pool, conv_pool, dims=dims)
+    d, n = _host_table(slots)
+    copy_slots([-1] * n, d, state_pool, conv_pool, dims=dims)
 
 
 def compact_slots(live, state_pool, conv_pool, *, clear: bool = False, dims: Dims = MODEL):
@@ -720,17 +740,12 @@ def compact_slots(live, state_pool, conv_pool, *, clear: bool = False, dims: Dim
     the live count stay, those behind it fill the free rows before it in ascending order.  ``clear``
     zeroes the rows behind.  Returns the new row of each old row, int32 on the host, -1 where not live."""
     dev, P = _pool_checked(state_pool, conv_pool, dims, "compact_slots")
-    flags = live.detach().to("cpu") if isinstance(live, torch.Tensor) else torch.tensor(list(live))
-    flags = (flags != 0).to(torch.uint8).contiguous()
-    if tuple(flags.shape) != (P,):
+    flags = bytes(map(bool, live.tolist() if isinstance(live, torch.Tensor) else live))
+    if len(flags) != P:
         raise ValueError("compact_slots: one flag per pool row")
     remap = torch.empty((P,), dtype=torch.int32)
-    dc = _dims_c(dims)
-    with torch.cuda.device(dev):
-        st = load_library().gdn_compact_slots(ctypes.byref(dc), P, ctypes.c_void_p(flags.data_ptr()), int(bool(clear)),
-                                              _ptr(state_pool), _ptr(conv_pool), ctypes.c_void_p(remap.data_ptr()),
-                                              _stream(dev))
-    _check(st, "gdn_compact_slots")
+    _check(_on(dev, load_library().gdn_compact_slots, ctypes.byref(_dims_of(dims)), P, flags, bool(clear),
+               state_pool.data_ptr(), conv_pool.data_ptr(), remap.data_ptr()), "gdn_compact_slots")
     return remap
 
 
