@@ -603,9 +603,9 @@ def in_proj_quant(x, w_in: QuantTensor, *, dims: Dims = MODEL, out=None):
     L = load_library()
     qkv, z, a, b = _proj_out(out, x, T, (C, VD, Vh, Vh), "in_proj_quant")
     ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
-    ws = x.new_empty((ws_bytes,), dtype=torch.uint8)
+    ws = x.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
     _check(_on(dev, L.gdn_in_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, K, x.data_ptr(), *ptrs, qkv.data_ptr(),
-               z.data_ptr(), b.data_ptr(), a.data_ptr(), ws.data_ptr(), ws_bytes), "gdn_in_proj_quant")
+               z.data_ptr(), b.data_ptr(), a.data_ptr(), _ptr(ws), ws_bytes), "gdn_in_proj_quant")
     return qkv, z, a, b
 
 
@@ -621,9 +621,9 @@ def out_proj_quant(y, w_out: QuantTensor, *, dims: Dims = MODEL, out=None):
     L = load_library()
     out, = _proj_out(None if out is None else [out], y, T, (hidden,), "out_proj_quant")
     ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
-    ws = y.new_empty((ws_bytes,), dtype=torch.uint8)
+    ws = y.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
     _check(_on(dev, L.gdn_out_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, hidden, y.data_ptr(), *ptrs,
-               out.data_ptr(), ws.data_ptr(), ws_bytes), "gdn_out_proj_quant")
+               out.data_ptr(), _ptr(ws), ws_bytes), "gdn_out_proj_quant")
     return out
 
 

@@ -1375,48 +1375,73 @@ int qproj_pairs(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, in
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, mSw, mSx, p));
 }
 
-template <int FMT, int BN>
-int qproj_few(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
-    using C = qproj::few::Cfg<BN>;
-    CUtensorMap mW, mX;
-    if (!make_code_map(&mW, cw, p.K, p.N, qproj::few::kTileN) || !make_code_map(&mX, cx, p.K, p.T, BN)) return GDN_ERR_CUDA;
-    auto kernel = gdn_qproj_few_kernel<FMT, BN>;
-    const int st = smem_optin(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES);
-    if (st != GDN_OK) return st;
-    // clusters that share a tile's K while the tiles leave SMs idle, at least two stages each
+// Clusters that share a tile's K while the tiles leave SMs idle, at least two stages each.
+int few_split(const qproj::Params& p, int nsm) {
     const int tiles = (p.N + qproj::few::kTileN - 1) / qproj::few::kTileN, steps = (p.K + qproj::BK - 1) / qproj::BK;
     int split = nsm / tiles;
     if (split > steps / 2) split = steps / 2;
     if (split > qproj::few::kMaxSplit) split = qproj::few::kMaxSplit;
-    if (split < 1) split = 1;
+    return split < 1 ? 1 : split;
+}
+
+template <int FMT, int BN, bool kFuse>
+int qproj_few(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
+    using C = qproj::few::Cfg<BN, kFuse>;
+    CUtensorMap mW, mX;
+    if (!make_code_map(&mW, cw, p.K, p.N, qproj::few::kTileN)) return GDN_ERR_CUDA;
+    if (kFuse) mX = mW;  // (not read)
+    else if (!make_code_map(&mX, cx, p.K, p.T, BN)) return GDN_ERR_CUDA;
+    auto kernel = gdn_qproj_few_kernel<FMT, BN, kFuse>;
+    const int st = smem_optin(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES);
+    if (st != GDN_OK) return st;
+    const int split = few_split(p, nsm);
     cudaLaunchAttribute attr[2];
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 1;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = split;
-    const cudaLaunchConfig_t cfg = after_quantize(dim3(tiles, 1, split), qproj::few::kThreads, C::SMEM_BYTES, stream, attr, split > 1 ? 2 : 1);
+    cudaLaunchConfig_t cfg = after_quantize(dim3((p.N + qproj::few::kTileN - 1) / qproj::few::kTileN, 1, split), C::kThreads,
+                                            C::SMEM_BYTES, stream, attr, split > 1 ? 2 : 1);
+    if (kFuse) {  // the call's only launch: an ordinary one
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = split > 1 ? 1 : 0;
+    }
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, p));
 }
 
+int sm_count(int* nsm) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+                   cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
 template <int FMT>
-int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, cudaStream_t stream) {
-    int dev = 0, nsm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return GDN_ERR_CUDA;
-    if (p.T <= 16) return qproj_few<FMT, 16>(cx, cw, p, nsm, stream);
-    if (p.T <= 32) return qproj_few<FMT, 32>(cx, cw, p, nsm, stream);
-    if (p.T <= 64) return qproj_few<FMT, 64>(cx, cw, p, nsm, stream);
-    if (p.T <= 128) return qproj_few<FMT, 128>(cx, cw, p, nsm, stream);
+int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
+    if (p.T <= 16) return qproj_few<FMT, 16, false>(cx, cw, p, nsm, stream);
+    if (p.T <= 32) return qproj_few<FMT, 32, false>(cx, cw, p, nsm, stream);
+    if (p.T <= 64) return qproj_few<FMT, 64, false>(cx, cw, p, nsm, stream);
+    if (p.T <= 128) return qproj_few<FMT, 128, false>(cx, cw, p, nsm, stream);
     return qproj_pairs<FMT>(cx, cw, p, nsm, stream);
 }
 
-// Workspace of a 4-bit projection: the quantised tokens.
+// Whether a projection quantises its few tokens itself: at most 16384 elements, which fit its threads'
+// registers, of rows that fit its shared memory.  In_proj of 5120 -> 16480, nvfp4, as a graph: 1 token 13.3 -> 11.9
+// us, 2 tokens 13.0 -> 12.3; every CTA repeating the quantisation of more costs more than the launch it saves (4
+// tokens 12.9 -> 14.2, 8 tokens 13.4 -> 16.3).
+bool few_fuse(int64_t T, int K) {
+    return T <= 16 && T * (K / quant::kUnit) <= qproj::few::kRowThreads * qproj::few::kHold &&
+           K <= qproj::few::kMaxSteps * qproj::BK;
+}
+
+// Workspace of a 4-bit projection: the quantised tokens, none where it quantises them itself.
 struct QuantRows {
     size_t off_scales, off_row_scale, bytes;
 };
 QuantRows quant_rows(int format, int64_t T, int K) {
     QuantRows q{};
+    if (few_fuse(T, K)) return q;
     q.off_scales = align_up((size_t)T * (K / 2));
     q.off_row_scale = q.off_scales + align_up(quant_scale_bytes(format, T, K));
     q.bytes = q.off_row_scale + align_up((size_t)T * 4);
@@ -1433,10 +1458,10 @@ int proj_quant(int format, int32_t T, int32_t K, int32_t N, const uint16_t* x, c
     for (int i = 0; i < nseg; ++i)
         if (seg[i].dst == nullptr || !aligned16(seg[i].dst)) return GDN_ERR_INVALID_ARG;
     const QuantRows q = quant_rows(format, T, K);
-    if (workspace == nullptr || workspace_bytes < q.bytes) return GDN_ERR_WORKSPACE;
+    if (workspace_bytes < q.bytes || (workspace == nullptr && q.bytes > 0)) return GDN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GDN_ERR_INVALID_ARG;
-    int st = check_device();
-    if (st != GDN_OK) return st;
+    int st = check_device(), nsm = 0;
+    if (st != GDN_OK || (st = sm_count(&nsm)) != GDN_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* wsb = static_cast<uint8_t*>(workspace);
     qproj::Params p{};
@@ -1444,17 +1469,21 @@ int proj_quant(int format, int32_t T, int32_t K, int32_t N, const uint16_t* x, c
     p.N = N;
     p.K = K;
     p.tiles = quant::scale_tiles(format, K);
+    p.x = x;
     p.sx = wsb + q.off_scales;
     p.sw = w_scales;
     p.gx = reinterpret_cast<const float*>(wsb + q.off_row_scale);
     p.gw = w_row_scale;
     p.nseg = nseg;
     for (int i = 0; i < nseg; ++i) p.seg[i] = seg[i];
+    if (few_fuse(T, K))
+        return format == GDN_NVFP4 ? qproj_few<quant::kNvfp4, 16, true>(nullptr, w_codes, p, nsm, s)
+                                   : qproj_few<quant::kMxfp4, 16, true>(nullptr, w_codes, p, nsm, s);
     if ((st = quantize_launch(format, T, K, x, wsb, wsb + q.off_scales,
                               reinterpret_cast<float*>(wsb + q.off_row_scale), s)) != GDN_OK)
         return st;
-    return format == GDN_NVFP4 ? qproj_launch<quant::kNvfp4>(wsb, w_codes, p, s)
-                                    : qproj_launch<quant::kMxfp4>(wsb, w_codes, p, s);
+    return format == GDN_NVFP4 ? qproj_launch<quant::kNvfp4>(wsb, w_codes, p, nsm, s)
+                                    : qproj_launch<quant::kMxfp4>(wsb, w_codes, p, nsm, s);
 }
 
 // ---------------------------------------------------------------- pool rows

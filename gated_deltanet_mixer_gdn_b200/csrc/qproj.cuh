@@ -68,6 +68,7 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 struct Params {
     int T, N, K;                 // tokens, output features, contraction width (a multiple of 64)
     int tiles;                   // scale tiles per row of either operand
+    const uint16_t* x;           // the tokens [T][K] bf16 (where the projection quantises them itself)
     const uint8_t *sx, *sw;      // block scales
     const float *gx, *gw;        // row scales [T], [N]
     int nseg;                    // output segments over the features, as in the bf16 projections
@@ -103,39 +104,110 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 namespace few {
 constexpr int kTileN = 128;                           // features per tile (rows of the A operand)
 constexpr uint32_t W_BYTES = kTileN * BK / 2;         // 16 KB
-constexpr int kThreads = 192;                         // warp 0 loads, warp 1 products, warps 2-5 epilogue
 constexpr int kMaxSplit = 8;                          // CTAs of a cluster that share a tile's K
+// The tokens quantised by the projection itself (kFuse): kRowThreads threads hold kHold units of 16 elements
+// each, and a CTA's part of K is at most kMaxSteps stages (its codes and scales stay in shared memory).
+constexpr int kRowThreads = 512, kHold = 2, kMaxSteps = 24;
 
-template <int BN>
+template <int BN, bool kFuse>
 struct Cfg {
     static constexpr uint32_t X_BYTES = BN * BK / 2;
-    static constexpr uint32_t STAGE_BYTES = W_BYTES + X_BYTES + 2 * S_BYTES;
-    static constexpr int kStages = BN <= 32 ? 9 : BN <= 64 ? 7 : 6;
-    static constexpr uint32_t OFF_MISC = kStages * STAGE_BYTES;
-    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 256 + 1024;
+    static constexpr uint32_t X_STAGE = X_BYTES + S_BYTES;  // a stage's token codes and scales
+    static constexpr uint32_t STAGE_BYTES = W_BYTES + S_BYTES + (kFuse ? 0 : X_STAGE);
+    static constexpr int kStages = kFuse ? 7 : BN <= 32 ? 9 : BN <= 64 ? 7 : 6;
+    static constexpr uint32_t OFF_X = kStages * STAGE_BYTES;  // (kFuse) all stages' tokens
+    static constexpr uint32_t OFF_MISC = OFF_X + (kFuse ? kMaxSteps * X_STAGE : 0);
+    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 512 + 1024;
+    static constexpr int kThreads = 64 + (kFuse ? kRowThreads : 128);  // warp 0 loads, warp 1 products, rows and sums
     // tensor memory: the sums (BN columns), then per stage 16 columns of weight scales and 16 of token
     // scales; a stage's columns are free when its shared memory is
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(BN + 32 * kStages <= 512, "tensor memory");
-    static_assert(X_BYTES % 1024 == 0, "swizzle atoms");
+    static_assert(X_BYTES % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    static_assert(OFF_MISC >= BN * kTileN * 4, "the partial sums reuse the ring");
+    static_assert(kStages * STAGE_BYTES >= BN * kTileN * 4, "the partial sums reuse the ring");
 };
 }  // namespace few
 }  // namespace qproj
 
+// (kFuse) The tokens' rows, held in registers by kRowThreads threads: row maxima, then the codes (swizzled
+// rows of 128 bytes per stage) and scale tiles of stages [k0, k0 + ksteps) into shared memory at `out`, and
+// the row scales over the maxima.  The same values as gdn_quantize_kernel's.
+template <int FMT, class C>
+__device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t* out, uint32_t* s_amax,
+                                                uint64_t* rows_ready, int tid, int k0, int ksteps) {
+    using namespace qproj;
+    using namespace qproj::few;
+    const int per_row = p.K / quant::kUnit, units = p.T * per_row;  // units <= kRowThreads * kHold
+    const uint32_t inv = (0xffffffffu / per_row) + 1;                 // u / per_row by the high word, exact below 2^16
+    auto row_of = [&](int u) { return static_cast<int>(per_row == 1 ? u : __umulhi(static_cast<uint32_t>(u), inv)); };
+    const uint4* src = reinterpret_cast<const uint4*>(p.x);
+    uint4 a[kHold], b[kHold];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const int u = tid + h * kRowThreads;
+        a[h] = b[h] = make_uint4(0, 0, 0, 0);
+        if (u < units) {
+            a[h] = __ldg(src + 2 * u);
+            b[h] = __ldg(src + 2 * u + 1);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        if (h * kRowThreads < units) {
+            const int u = tid + h * kRowThreads, u0 = u & ~31;
+            const uint32_t um = quant::amax_bits16(a[h], b[h]);
+            if (u0 < units && row_of(u0) == row_of(min(u0 + 31, units - 1))) {  // the warp's units are in one row
+                const uint32_t wm = __reduce_max_sync(0xffffffffu, um);
+                if ((tid & 31) == 0) atomicMax(&s_amax[row_of(u0)], wm);
+            } else if (u < units) {
+                atomicMax(&s_amax[row_of(u)], um);
+            }
+        }
+    }
+    named_barrier_sync(1, kRowThreads);
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const int u = tid + h * kRowThreads;
+        if (h * kRowThreads < units) {  // (whole warps: blocks of two units exchange their maxima)
+            const int t = u < units ? row_of(u) : 0, ku = u - t * per_row;
+            uint32_t um = quant::amax_bits16(a[h], b[h]);
+            if constexpr (FMT == quant::kMxfp4) um = max(um, __shfl_xor_sync(0xffffffffu, um, 1));
+            const int stage = ku / (BK / quant::kUnit) - k0;
+            if (u < units && stage >= 0 && stage < ksteps) {
+                uint2 codes;
+                uint32_t scale;
+                quant::quantize_unit<FMT>(a[h], b[h], um, s_amax[t], codes, scale);
+                uint8_t* st = out + stage * C::X_STAGE;
+                const int in = ku % (BK / quant::kUnit);  // the unit's 8 bytes in the stage's 128
+                *reinterpret_cast<uint2*>(st + sw128_chunk(t, in >> 1) + 8 * (in & 1)) = codes;
+                const int blk = in / (quant::block_of(FMT) / quant::kUnit);
+                if (FMT == quant::kNvfp4 || (in & 1) == 0)
+                    st[C::X_BYTES + (blk >> 2) * quant::kTileBytes + t * 16 + (blk & 3)] = static_cast<uint8_t>(scale);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(rows_ready);
+    named_barrier_sync(1, kRowThreads);  // the maxima have been read
+    if (tid < p.T) s_amax[tid] = __float_as_uint(quant::row_scale_of<FMT>(s_amax[tid]));
+}
+
 // At most 128 tokens: a tile is 128 features x all BN (>= T) tokens, the weights the A operand, so that few
 // tokens still fill the tensor core's 128 lanes.  Bound: reading the weights once.  Where the tiles are fewer
 // than the SMs a cluster of gridDim.z CTAs shares one tile's K; each leaves its sums in shared memory and adds
-// the others' for its part of the tokens, in rank order.  The loads of the first stages' weights, and all of
-// the prologue, run before the quantisation of the tokens (the previous launch of the call) is waited for.
-template <int FMT, int BN>
-__global__ void __launch_bounds__(qproj::few::kThreads, 1)
+// the others' for its part of the tokens, in rank order.
+// kFuse (few elements in all): every CTA quantises the tokens itself, its part of K into shared memory, while
+// its weights arrive: no second launch (3 us) and no workspace; all CTAs repeat the work, so it stays at what
+// their registers hold.  Else the tokens were quantised by the call's previous launch, and the loads of the
+// first stages' weights, and all of the prologue, run before its end is waited for.
+template <int FMT, int BN, bool kFuse>
+__global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
     gdn_qproj_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                          const qproj::Params p) {
     using namespace qproj;
     using namespace qproj::few;
-    using C = Cfg<BN>;
+    using C = Cfg<BN, kFuse>;
     constexpr int kTiles = kTilesPerStage(FMT);
     constexpr uint32_t ID = idesc(FMT, kTileN, BN);
     extern __shared__ uint8_t smem_raw[];
@@ -144,7 +216,9 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
     uint64_t* empty = full + C::kStages;
     uint64_t* done = empty + C::kStages;
+    uint64_t* rows_ready = done + 1;  // (kFuse) the tokens' codes and scales are in shared memory
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 192);
+    uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);  // (kFuse) [BN], then row scales
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n0 = blockIdx.x * kTileN;
     const int split = gridDim.z, rank = blockIdx.z;  // (the cluster spans z)
@@ -158,10 +232,12 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
+        mbar_init(rows_ready, kRowThreads);
         fence_barrier_init();
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
+    if (kFuse && tid < BN) s_amax[tid] = 0;
     if (warp == 1) {
         tmem_alloc(s_tmem, C::TMEM_COLS);
         tmem_relinquish();
@@ -183,22 +259,23 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
         auto scale_bytes = [&](int ks) { return min(kTiles, p.tiles - (k0 + ks) * kTiles) * quant::kTileBytes; };
         auto load_w = [&](int ks, int s) {
             uint8_t* st = smem + s * C::STAGE_BYTES;
-            mbar_arrive_expect_tx(&full[s], W_BYTES + C::X_BYTES + 2 * scale_bytes(ks));
+            mbar_arrive_expect_tx(&full[s], W_BYTES + (kFuse ? 0 : C::X_BYTES) + (kFuse ? 1 : 2) * scale_bytes(ks));
             tma_load_2d(st, &tmW, (k0 + ks) * (BK / 2), n0, &full[s]);
-            bulk_load(st + W_BYTES + C::X_BYTES,
+            bulk_load(st + W_BYTES,
                       p.sw + ((size_t)blockIdx.x * p.tiles + (k0 + ks) * kTiles) * quant::kTileBytes, scale_bytes(ks), &full[s]);
         };
         auto load_x = [&](int ks, int s) {
-            uint8_t* st = smem + s * C::STAGE_BYTES;
-            tma_load_2d(st + W_BYTES, &tmX, (k0 + ks) * (BK / 2), 0, &full[s]);
-            bulk_load(st + W_BYTES + C::X_BYTES + S_BYTES, p.sx + (size_t)(k0 + ks) * kTiles * quant::kTileBytes,
+            if (kFuse) return;
+            uint8_t* st = smem + s * C::STAGE_BYTES + W_BYTES + S_BYTES;
+            tma_load_2d(st, &tmX, (k0 + ks) * (BK / 2), 0, &full[s]);
+            bulk_load(st + C::X_BYTES, p.sx + (size_t)(k0 + ks) * kTiles * quant::kTileBytes,
                       scale_bytes(ks), &full[s]);
         };
         const int head = min(C::kStages, ksteps);
         if (elect_one())
             for (int ks = 0; ks < head; ++ks) load_w(ks, ks);
         __syncwarp();
-        grid_wait();
+        if (!kFuse) grid_wait();
         if (elect_one())
             for (int ks = 0; ks < head; ++ks) load_x(ks, ks);
         __syncwarp();
@@ -220,13 +297,15 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
     } else if (warp == 1) {
         const uint64_t kDesc = sw128_desc(0, 16, 1024), sDesc = scale_desc(0);
         uint32_t s = 0, ph = 0;
+        if (kFuse) wait1(rows_ready, 0, kErrTimeoutTma);
         for (int ks = 0; ks < ksteps; ++ks) {
             wait1(&full[s], ph, kErrTimeoutTma);
             if (broken) break;
             tc_fence_after();
             const uint32_t aW = sbase + s * C::STAGE_BYTES;
-            const uint64_t dW = desc_at(kDesc, aW), dX = desc_at(kDesc, aW + W_BYTES);
-            const uint64_t dS = desc_at(sDesc, aW + W_BYTES + C::X_BYTES);
+            const uint32_t aX = kFuse ? sbase + C::OFF_X + ks * C::X_STAGE : aW + W_BYTES + S_BYTES;
+            const uint64_t dW = desc_at(kDesc, aW), dX = desc_at(kDesc, aX);
+            const uint64_t dSw = desc_at(sDesc, aW + W_BYTES), dSx = desc_at(sDesc, aX + C::X_BYTES);
             const uint32_t cW = tbase + BN + 32 * s, cX = cW + 16;
             const int nk = min(BK / kMmaK, (p.K - (k0 + ks) * BK) / kMmaK);
             const uint32_t more = ks > 0;
@@ -234,8 +313,8 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
                 // (at the end of K some tiles hold an earlier stage's scales: no product reads them)
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
-                    copy_scales(cW + 4 * i, dS + 32 * i);
-                    copy_scales(cX + 4 * i, dS + (S_BYTES >> 4) + 32 * i);
+                    copy_scales(cW + 4 * i, dSw + 32 * i);
+                    copy_scales(cX + 4 * i, dSx + 32 * i);
                 }
 #pragma unroll
                 for (int kk = 0; kk < BK / kMmaK; ++kk) {
@@ -252,14 +331,16 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
             if (++s == C::kStages) s = 0, ph ^= 1;
         }
     } else {
+        if constexpr (kFuse) quantize_tokens<FMT, C>(p, smem + C::OFF_X, s_amax, rows_ready, tid - 64, k0, ksteps);
         // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
         float* part = reinterpret_cast<float*>(smem);
         wait1(done, 0, kErrTimeoutMma);
         __syncwarp();
         tc_fence_after();
+        constexpr int kWays = (C::kThreads - 64) / 128;  // warps per lane quarter
 #pragma unroll 1
-        for (int j = 0; j < BN / 16; ++j) {
+        for (int j = (warp - 2) >> 2; j < BN / 16; j += kWays) {
             float v[16];
             tmem_ld16(tbase + (static_cast<uint32_t>(32 * q4) << 16) + 16 * j, v);
             tmem_ld_wait();
@@ -272,7 +353,7 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
     else __syncthreads();
     if (warp >= 2) {
         // ---------------- this rank's tokens: four features per lane, a token's 128 per warp
-        grid_wait();  // the tokens' row scales
+        if (!kFuse) grid_wait();  // the tokens' row scales
         const int n = n0 + 4 * lane;
         float gw[4];
 #pragma unroll
@@ -281,7 +362,7 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
         const GemmSegment g = segment_of(p, n, end);
         const bool whole = n + 4 <= end && (((n - g.col0) | g.ld) & 3) == 0;  // (segments start on 16 bytes)
         const uint32_t mine = sbase + 16 * lane;
-        for (int t = rank + split * (warp - 2); t < p.T; t += 4 * split) {
+        for (int t = rank + split * (warp - 2); t < p.T; t += (C::kThreads / 32 - 2) * split) {
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int r = 0; r < split; ++r) {
                 float4 b;
@@ -296,7 +377,7 @@ __global__ void __launch_bounds__(qproj::few::kThreads, 1)
                 a.z += b.z;
                 a.w += b.w;
             }
-            const float gx = __ldg(p.gx + t);
+            const float gx = kFuse ? __uint_as_float(s_amax[t]) : __ldg(p.gx + t);
             const uint32_t lo = pack_bf16x2(a.x * (gx * gw[0]), a.y * (gx * gw[1]));
             const uint32_t hi = pack_bf16x2(a.z * (gx * gw[2]), a.w * (gx * gw[3]));
             if (whole) {

@@ -83,6 +83,15 @@ __device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) 
 // keeps the sign of a zero).
 __device__ __forceinline__ float snap16(float v) { return __uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u); }
 
+// A row's scale from its largest magnitude (bf16 bits).
+template <int FMT>
+__device__ __forceinline__ float row_scale_of(uint32_t row_max) {
+    if (row_max >= 0x7f80u) return __uint_as_float(0x7fc00000u);
+    if (FMT != kNvfp4) return 1.0f;
+    // amax = (1 + m / 128) 2^e against 2688 = (1 + 40 / 128) 2^11
+    return pow2f(max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100));
+}
+
 // The 16 codes of one thread's unit and its block's scale byte, from the unit, the block's and the
 // row's largest magnitudes.
 template <int FMT>
@@ -91,7 +100,6 @@ __device__ __forceinline__ void quantize_unit(const uint4& a, const uint4& b, ui
     const bool finite = row_max < 0x7f80u;
     float inv;  // 1 / (s g)
     if constexpr (FMT == kNvfp4) {
-        // amax = (1 + m / 128) 2^e against 2688 = (1 + 40 / 128) 2^11
         const int j = max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100);
         const float inv_g = pow2f(-j);
         scale = e4m3_bits(snap16(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g * (1.0f / 6.0f)));
@@ -217,12 +225,7 @@ __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const qu
             }
             emit(u, ua, ub, amax_bits16(ua, ub));
         }
-        if (threadIdx.x == 0) {
-            float gs = 1.0f;
-            if (FMT == kNvfp4)
-                gs = pow2f(max(static_cast<int>(rm >> 7) - 127 - 11 + ((rm & 127u) > 40u ? 1 : 0), -100));
-            p.row_scale[row] = rm < 0x7f80u ? gs : __uint_as_float(0x7fc00000u);
-        }
+        if (threadIdx.x == 0) p.row_scale[row] = row_scale_of<FMT>(rm);
     }
 }
 

@@ -61,15 +61,20 @@ def test_projection_arguments(lib):
     assert lib.gdn_in_proj_quant(_dims(), 0, 0, 128, *([None] * 9), 0, None) == 0
     assert lib.gdn_out_proj_quant(_dims(), 1, 0, 128, *([None] * 6), 0, None) == 0
     assert lib.gdn_out_proj_quant(_dims(), 1, 8, 0, *ok_out) == -1
-    need = lib.gdn_proj_quant_workspace_size(0, 8, 128)
-    assert lib.gdn_in_proj_quant(_dims(), 0, 8, 128, *ok_in[:9], need - 1, None) == -4
+    need = lib.gdn_proj_quant_workspace_size(0, 100, 128)
+    assert need >= 100 * 64 + 2 * 512 + 400
+    assert lib.gdn_in_proj_quant(_dims(), 0, 100, 128, *ok_in[:9], need - 1, None) == -4
+    # a few tokens are quantised on chip, while they fit there
+    assert lib.gdn_proj_quant_workspace_size(0, 2, 6144) == 0 and lib.gdn_proj_quant_workspace_size(1, 16, 1024) == 0
+    for T, K in ((3, 6144), (16, 1088), (17, 64), (1, 6208)):
+        assert lib.gdn_proj_quant_workspace_size(0, T, K) >= T * (K // 2 + K // 16 + 4)
     for fn, ok, n, extra in ((lib.gdn_in_proj_quant, ok_in, 9, 128), (lib.gdn_out_proj_quant, ok_out, 6, 64)):
         for i in range(n):
             for bad in (None, 10):
                 args = list(ok)
                 args[i] = bad
                 want = -4 if i == n - 1 and bad is None else -1
-                assert fn(_dims(), 0, 8, extra, *args) == want, (fn, i, bad)
+                assert fn(_dims(), 0, 100, extra, *args) == want, (fn, i, bad)
 
 
 def _table(*rows):
