@@ -404,8 +404,9 @@ constexpr uint32_t OFF_MISC = kStages * STAGE_BYTES;
 constexpr uint32_t OFF_GW = OFF_MISC + 256;           // the tile's feature row scales, two buffers
 constexpr uint32_t kOutBytes = 32 * 128;              // a warp's 32 tokens x 64 features on their way out
 constexpr uint32_t OFF_OUT = OFF_GW + 2 * kTileN * 4;
-constexpr uint32_t SMEM_BYTES = OFF_OUT + 4 * kOutBytes + 1024;
-constexpr int kDuoThreads = 192;                      // warp 0 loads, warp 1 products, warps 2-5 epilogue
+constexpr uint32_t SMEM_BYTES = OFF_OUT + 8 * kOutBytes + 1024;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+constexpr int kDuoThreads = 320;                      // warp 0 loads, warp 1 products, warps 2-9 epilogue
 // Tensor memory: two accumulators of 256 columns that share columns [kAcc1, 256), and two buffers of
 // scales behind them (16 columns of token scales, 32 of feature scales each).
 constexpr uint32_t kAcc1 = 160, kScales = kAcc1 + kTileN, kScaleCols = 48;
@@ -494,9 +495,22 @@ __device__ __forceinline__ void store_tile32x64(const Params& p, int t0, int c0,
         }
     } else if (t0 + lane < p.T) {  // segment boundaries, the last features, rows off 16 bytes
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-            const uint32_t w = e < 32 ? lo[(e & 31) >> 1] : hi[(e & 31) >> 1];
-            if (c0 + e < p.N) *output_at(p, c0 + e, t0 + lane) = static_cast<uint16_t>(e & 1 ? w >> 16 : w);
+        for (int c = 0; c < 8; ++c) {
+            const int n = c0 + 8 * c;
+            if (n >= p.N) break;
+            const uint32_t(&w)[16] = c < 4 ? lo : hi;
+            const GemmSegment sg = segment_of(p, n, end);
+            uint16_t* dst = sg.dst + (size_t)(t0 + lane) * sg.ld + (n - sg.col0);
+            if (n + 8 <= end && (((n - sg.col0) | sg.ld) & 7) == 0) {
+                *reinterpret_cast<uint4*>(dst) =
+                    make_uint4(w[4 * (c & 3)], w[4 * (c & 3) + 1], w[4 * (c & 3) + 2], w[4 * (c & 3) + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (n + e < p.N)
+                        *output_at(p, n + e, t0 + lane) =
+                            static_cast<uint16_t>(w[4 * (c & 3) + (e >> 1)] >> (16 * (e & 1)));
+            }
         }
     }
     __syncwarp();
@@ -548,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
         }
         mbar_init(&acc_full[0], 1);
         mbar_init(&acc_full[1], 1);
-        mbar_init(acc_free, 8);  // the epilogue warps of both CTAs
+        mbar_init(acc_free, 16);  // the epilogue warps of both CTAs
         fence_barrier_init();
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
@@ -661,6 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
     } else {
         // ---------------- epilogue: this CTA's 128 tokens
         const int q4 = warp & 3, et = tid - 64;
+        const bool upper = warp >= 6;  // two warps per lane quarter share the tile's columns
         const uint32_t tl = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t free_bar = cluster_addr(acc_free, 0);
         grid_wait();
@@ -670,20 +685,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             coords(t, tm, tn);
             const int row = tm * kTileM + 128 * rank + 32 * q4 + lane, n0 = tn * kTileN;
             float* gw = s_gw + (it & 1) * kTileN;
-            for (int i = et; i < kTileN; i += 128) gw[i] = n0 + i < p.N ? __ldg(p.gw + n0 + i) : 0.0f;
+            for (int i = et; i < kTileN; i += 256) gw[i] = n0 + i < p.N ? __ldg(p.gw + n0 + i) : 0.0f;
             const float gx = row < p.T ? __ldg(p.gx + row) : 0.0f;
-            named_barrier_sync(1, 128);
+            named_barrier_sync(1, 256);
             wait1(&acc_full[it & 1], (it >> 1) & 1, kErrTimeoutMma);
             __syncwarp();
             tc_fence_after();
             const uint32_t acc = tbase + tl + ((it & 1) ? kAcc1 : 0);
-            // the shared columns first, into registers, and the next tile's products may start: columns
-            // 160 .. 255 of the first accumulator, 0 .. 95 of the second
-            const int shared0 = (it & 1) ? 0 : kAcc1;
-            float v0[32], v1[32], v2[32];
-            tmem_ld32(acc + shared0, v0);
-            tmem_ld32(acc + shared0 + 32, v1);
-            tmem_ld32(acc + shared0 + 64, v2);
+            // the shared columns first, into registers, and the next tile's products may start: columns 160 .. 255
+            // of the first accumulator, 0 .. 95 of the second.  A warp stores its columns in two parts of 64: one
+            // that holds its shared columns, then one that holds none.
+            const bool second = (it & 1) != 0;
+            const int part0 = second ? (upper ? 0 : 64) : (upper ? 192 : 128);
+            const int part1 = (second ? 128 : 0) + (upper ? 64 : 0);
+            float v0[32], v1[32];
+            if (upper) {  // all 64 of its first part are shared
+                tmem_ld32(acc + part0, v0);
+                tmem_ld32(acc + part0 + 32, v1);
+            } else {      // 32 are: its last (160 .. 191) or first (64 .. 95)
+                tmem_ld32(acc + part0 + (second ? 0 : 32), v0);
+            }
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -695,35 +716,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             const int t0 = row - lane;
             uint32_t lo[16], hi[16];
             auto from_tmem = [&](int c, uint32_t(&o)[16]) {
-                tmem_ld32(acc + c, v0);
+                tmem_ld32(acc + c, v1);
                 tmem_ld_wait();
-                scale_pack32(v0, gx, gw + c, o);
+                scale_pack32(v1, gx, gw + c, o);
             };
             auto emit = [&](int c) {
                 if (n0 + c < p.N) store_tile32x64(p, t0, n0 + c, lo, hi, stage, lane);
             };
-            const bool second = (it & 1) != 0;  // the accumulator with the shared columns at its start
-            if (second) {
-                scale_pack32(v0, gx, gw, lo);
-                scale_pack32(v1, gx, gw + 32, hi);
-                emit(0);
-                scale_pack32(v2, gx, gw + 64, lo);
-                from_tmem(96, hi);
-                emit(64);
+            if (upper) {
+                scale_pack32(v0, gx, gw + part0, lo);
+                scale_pack32(v1, gx, gw + part0 + 32, hi);
+            } else if (second) {
+                scale_pack32(v0, gx, gw + part0, lo);
+                from_tmem(part0 + 32, hi);
             } else {
-                scale_pack32(v1, gx, gw + 192, lo);
-                scale_pack32(v2, gx, gw + 224, hi);
-                emit(192);
-                scale_pack32(v0, gx, gw + 160, hi);
-                from_tmem(128, lo);
-                emit(128);
+                scale_pack32(v0, gx, gw + part0 + 32, hi);
+                from_tmem(part0, lo);
             }
-#pragma unroll 1
-            for (int c = second ? 128 : 0; c < (second ? 256 : 128); c += 64) {
-                from_tmem(c, lo);
-                from_tmem(c + 32, hi);
-                emit(c);
-            }
+            emit(part0);
+            from_tmem(part1, lo);
+            from_tmem(part1 + 32, hi);
+            emit(part1);
         }
     }
     tc_fence_before();
