@@ -1496,7 +1496,8 @@ int pool_flush(pool::Params& p, int nsm, cudaStream_t stream) {
     if (p.nset == 0) return GDN_OK;
     int st = smem_optin(reinterpret_cast<const void*>(gdn_pool_kernel), pool::SMEM_BYTES);
     if (st != GDN_OK) return st;
-    gdn_pool_kernel<<<p.ntask < nsm ? p.ntask : nsm, 32, pool::SMEM_BYTES, stream>>>(p);
+    const int ctas = pool::kCtasPerSm * nsm;
+    gdn_pool_kernel<<<p.ntask < ctas ? p.ntask : ctas, 32, pool::SMEM_BYTES, stream>>>(p);
     p.nset = p.ntask = 0;
     return cuda_status(cudaGetLastError());
 }
@@ -1552,10 +1553,19 @@ int pool_launch(const gdn_dims* dims, std::vector<RowPair> pairs, int32_t pool_r
     p.row_bytes[0] = (uint32_t)dims->num_v_heads * 128 * 128 * 4;
     p.row_bytes[1] = 3u * (2 * dims->num_k_heads + dims->num_v_heads) * 128 * 4;
     p.pool_rows = pool_rows;
-    // a row's bytes per task: whole stages when the rows fill the device several times over, else
-    // smaller ranges so that every SM has some
-    const uint64_t total = (uint64_t)n * (p.row_bytes[0] + p.row_bytes[1]);
-    const uint32_t stage = total >= (uint64_t)nsm * pool::kStages * pool::kStageBytes ? pool::kStageBytes : 8192;
+    // Bytes loaded per task: what gives every CTA one task, up to a whole stage (a fork of one 27B row to four 5.2 ->
+    // 4.1 us against 8 KB tasks, of which some CTAs had two).
+    uint64_t loads = 0;  // rows loaded (or cleared, in a set that loads none)
+    for (size_t i = 0; i < n; i = set_end(i)) {
+        uint64_t distinct = 0;
+        for (size_t k = i; k < set_end(i); ++k) {
+            const int32_t src = pairs[key[k].second].src;
+            distinct += src >= 0 && (k == i || src != pairs[key[k - 1].second].src);
+        }
+        loads += distinct > 0 ? distinct : 1;
+    }
+    const uint64_t share = loads * (p.row_bytes[0] + p.row_bytes[1]) / ((uint64_t)pool::kCtasPerSm * nsm);
+    const uint32_t stage = share >= pool::kStageBytes ? pool::kStageBytes : share < 4096 ? 4096 : ((uint32_t)share + 127) & ~127u;
     int nsrc = 0, nop = 0;
     for (size_t i = 0; i < n;) {
         size_t j = set_end(i);
