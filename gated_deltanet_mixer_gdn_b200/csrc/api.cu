@@ -1273,6 +1273,14 @@ int gdn_version(void) { return 100; }
 namespace {
 
 // ---------------------------------------------------------------- 4-bit operands
+int sm_count(int* nsm) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+                   cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
 int check_format(int32_t format) {
     return format == GDN_NVFP4 || format == GDN_MXFP4 ? GDN_OK : GDN_ERR_INVALID_ARG;
 }
@@ -1284,17 +1292,16 @@ size_t quant_scale_bytes(int format, int64_t rows, int K) {
     return (size_t)((rows + 127) / 128) * quant::scale_tiles(format, K) * quant::kTileBytes;
 }
 
-// Launch shape of the row kernels: one unit of 16 elements per thread up to 512 threads a row (then two or
-// more), at least 256 threads a CTA, as many CTAs as the device holds at 2048 threads an SM.
-int quant_shape(int32_t rows, int32_t K, dim3* grid, dim3* block) {
-    int dev = 0, nsm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return GDN_ERR_CUDA;
-    const int units = K / quant::kUnit;
+// Launch shape of the row kernels: one unit (of `unit` elements) per thread up to 512 threads a row (then two or
+// more), at least 160 threads a CTA, `threads` of them per SM over the persistent grid.
+int quant_shape(int32_t rows, int32_t K, int unit, int threads, dim3* grid, dim3* block) {
+    int nsm = 0;
+    const int st = sm_count(&nsm);
+    if (st != GDN_OK) return st;
+    const int units = K / unit;
     const int gx = units >= quant::kMaxGroup ? quant::kMaxGroup : (units + 31) / 32 * 32;
-    const int gy = gx >= 256 ? 1 : 256 / gx;
-    const int64_t groups = ((int64_t)rows + gy - 1) / gy, resident = (int64_t)nsm * (2048 / (gx * gy));
+    const int gy = gx > 128 ? 1 : 256 / gx;
+    const int64_t groups = ((int64_t)rows + gy - 1) / gy, resident = (int64_t)nsm * (threads / (gx * gy));
     *block = dim3(gx, gy);
     *grid = dim3((unsigned)(groups < resident ? groups : resident));
     return GDN_OK;
@@ -1304,12 +1311,9 @@ int quantize_launch(int format, int32_t rows, int32_t K, const uint16_t* x, uint
                     float* row_scale, cudaStream_t stream) {
     const quant::Params p{x, codes, scales, row_scale, rows, K, quant::scale_tiles(format, K)};
     dim3 grid, block;
-    const int st = quant_shape(rows, K, &grid, &block);
+    const int st = quant_shape(rows, K, quant::kUnit, 2048, &grid, &block);
     if (st != GDN_OK) return st;
-    const bool two = K > quant::kMaxGroup * quant::kUnit;
-    auto kernel = format == GDN_NVFP4
-                      ? (two ? gdn_quantize_kernel<quant::kNvfp4, 2> : gdn_quantize_kernel<quant::kNvfp4, 1>)
-                      : (two ? gdn_quantize_kernel<quant::kMxfp4, 2> : gdn_quantize_kernel<quant::kMxfp4, 1>);
+    auto kernel = format == GDN_NVFP4 ? gdn_quantize_kernel<quant::kNvfp4> : gdn_quantize_kernel<quant::kMxfp4>;
     kernel<<<grid, block, 0, stream>>>(p);
     return cuda_status(cudaGetLastError());
 }
@@ -1409,14 +1413,6 @@ int qproj_few(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int 
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, p));
 }
 
-int sm_count(int* nsm) {
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess &&
-                   cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
-               ? GDN_OK
-               : GDN_ERR_CUDA;
-}
-
 template <int FMT>
 int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int nsm, cudaStream_t stream) {
     if (p.T <= 16) return qproj_few<FMT, 16, false>(cx, cw, p, nsm, stream);
@@ -1431,7 +1427,7 @@ int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, i
 // us, 2 tokens 13.0 -> 12.3; every CTA repeating the quantisation of more costs more than the launch it saves (4
 // tokens 12.9 -> 14.2, 8 tokens 13.4 -> 16.3).
 bool few_fuse(int64_t T, int K) {
-    return T <= 16 && T * (K / quant::kUnit) <= qproj::few::kRowThreads * qproj::few::kHold &&
+    return T <= 16 && T * (K / 16) <= qproj::few::kRowThreads * qproj::few::kHold &&
            K <= qproj::few::kMaxSteps * qproj::BK;
 }
 
@@ -1641,7 +1637,7 @@ int gdn_dequantize(int32_t format, int32_t rows, int32_t K, const uint8_t* codes
     if ((st = check_device()) != GDN_OK) return st;
     const int tiles = quant::scale_tiles(format, K);
     dim3 grid, block;
-    if ((st = quant_shape(rows, K, &grid, &block)) != GDN_OK) return st;
+    if ((st = quant_shape(rows, K, 16, 1280, &grid, &block)) != GDN_OK) return st;
     auto kernel = format == GDN_NVFP4 ? gdn_dequantize_kernel<quant::kNvfp4> : gdn_dequantize_kernel<quant::kMxfp4>;
     kernel<<<grid, block, 0, static_cast<cudaStream_t>(stream)>>>(codes, scales, row_scale, rows, K, tiles, out);
     return cuda_status(cudaGetLastError());

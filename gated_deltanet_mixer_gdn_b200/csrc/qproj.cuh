@@ -117,7 +117,7 @@ struct Cfg {
     static constexpr int kStages = kFuse ? 7 : BN <= 32 ? 9 : BN <= 64 ? 7 : 6;
     static constexpr uint32_t OFF_X = kStages * STAGE_BYTES;  // (kFuse) all stages' tokens
     static constexpr uint32_t OFF_MISC = OFF_X + (kFuse ? kMaxSteps * X_STAGE : 0);
-    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 512 + 1024;
+    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 256 + BN * 4 + 1024;
     static constexpr int kThreads = 64 + (kFuse ? kRowThreads : 128);  // warp 0 loads, warp 1 products, rows and sums
     // tensor memory: the sums (BN columns), then per stage 16 columns of weight scales and 16 of token
     // scales; a stage's columns are free when its shared memory is
@@ -138,7 +138,7 @@ __device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t*
                                                 uint64_t* rows_ready, int tid, int k0, int ksteps) {
     using namespace qproj;
     using namespace qproj::few;
-    const int per_row = p.K / quant::kUnit, units = p.T * per_row;  // units <= kRowThreads * kHold
+    const int per_row = p.K / 16, units = p.T * per_row;  // units <= kRowThreads * kHold
     const uint32_t inv = (0xffffffffu / per_row) + 1;                 // u / per_row by the high word, exact below 2^16
     auto row_of = [&](int u) { return static_cast<int>(per_row == 1 ? u : __umulhi(static_cast<uint32_t>(u), inv)); };
     const uint4* src = reinterpret_cast<const uint4*>(p.x);
@@ -173,15 +173,17 @@ __device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t*
             const int t = u < units ? row_of(u) : 0, ku = u - t * per_row;
             uint32_t um = quant::amax_bits16(a[h], b[h]);
             if constexpr (FMT == quant::kMxfp4) um = max(um, __shfl_xor_sync(0xffffffffu, um, 1));
-            const int stage = ku / (BK / quant::kUnit) - k0;
+            const int stage = ku / (BK / 16) - k0;
             if (u < units && stage >= 0 && stage < ksteps) {
-                uint2 codes;
+                const uint32_t rm = s_amax[t];
                 uint32_t scale;
-                quant::quantize_unit<FMT>(a[h], b[h], um, s_amax[t], codes, scale);
+                const float inv = quant::block_scale<FMT>(um, FMT == quant::kNvfp4 ? quant::inv_row_scale(rm) : 1.0f, scale);
+                uint2 codes = quant::codes16<FMT>(a[h], b[h], inv);
+                if (rm >= 0x7f80u) codes = make_uint2(0u, 0u), scale = 0u;
                 uint8_t* st = out + stage * C::X_STAGE;
-                const int in = ku % (BK / quant::kUnit);  // the unit's 8 bytes in the stage's 128
+                const int in = ku % (BK / 16);  // the unit's 8 bytes in the stage's 128
                 *reinterpret_cast<uint2*>(st + sw128_chunk(t, in >> 1) + 8 * (in & 1)) = codes;
-                const int blk = in / (quant::block_of(FMT) / quant::kUnit);
+                const int blk = in / (quant::block_of(FMT) / 16);
                 if (FMT == quant::kNvfp4 || (in & 1) == 0)
                     st[C::X_BYTES + (blk >> 2) * quant::kTileBytes + t * 16 + (blk & 3)] = static_cast<uint8_t>(scale);
             }
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
     uint64_t* done = empty + C::kStages;
     uint64_t* rows_ready = done + 1;  // (kFuse) the tokens' codes and scales are in shared memory
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 192);
-    uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);  // (kFuse) [BN], then row scales
+    float* s_gx = reinterpret_cast<float*>(smem + C::OFF_MISC + 256);          // [BN] the tokens' row scales
+    uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_gx);                      // (kFuse) their maxima before
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n0 = blockIdx.x * kTileN;
     const int split = gridDim.z, rank = blockIdx.z;  // (the cluster spans z)
@@ -335,6 +338,10 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
         float* part = reinterpret_cast<float*>(smem);
+        if constexpr (!kFuse) {
+            grid_wait();
+            if (tid - 64 < p.T) s_gx[tid - 64] = __ldg(p.gx + tid - 64);  // (T <= BN <= 128 threads)
+        }
         wait1(done, 0, kErrTimeoutMma);
         __syncwarp();
         tc_fence_after();
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
     else __syncthreads();
     if (warp >= 2) {
         // ---------------- this rank's tokens: four features per lane, a token's 128 per warp
-        if (!kFuse) grid_wait();  // the tokens' row scales
+        constexpr int kWarps = C::kThreads / 32 - 2, kBatch = 4;  // a warp's tokens, kBatch of them at once
         const int n = n0 + 4 * lane;
         float gw[4];
 #pragma unroll
@@ -361,31 +368,46 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         int end;
         const GemmSegment g = segment_of(p, n, end);
         const bool whole = n + 4 <= end && (((n - g.col0) | g.ld) & 3) == 0;  // (segments start on 16 bytes)
-        const uint32_t mine = sbase + 16 * lane;
-        for (int t = rank + split * (warp - 2); t < p.T; t += (C::kThreads / 32 - 2) * split) {
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int r = 0; r < split; ++r) {
-                float4 b;
-                uint32_t at = mine + t * kTileN * 4;
-                if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(r));
-                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
-                             : "r"(at)
-                             : "memory");
-                a.x += b.x;
-                a.y += b.y;
-                a.z += b.z;
-                a.w += b.w;
-            }
-            const float gx = kFuse ? __uint_as_float(s_amax[t]) : __ldg(p.gx + t);
-            const uint32_t lo = pack_bf16x2(a.x * (gx * gw[0]), a.y * (gx * gw[1]));
-            const uint32_t hi = pack_bf16x2(a.z * (gx * gw[2]), a.w * (gx * gw[3]));
-            if (whole) {
-                *reinterpret_cast<uint2*>(g.dst + (size_t)t * g.ld + (n - g.col0)) = make_uint2(lo, hi);
-            } else {
+        for (int t0 = rank + split * (warp - 2); t0 < p.T; t0 += kBatch * kWarps * split) {
+            float4 a[kBatch];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < p.N) *output_at(p, n + e, t) = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+            for (int i = 0; i < kBatch; ++i) a[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int r = 0; r < split; ++r) {
+                uint32_t at = sbase + 16 * lane;
+                if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(r));
+                float4 b[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {  // (past the last token: the last token's, not stored)
+                    const int t = min(t0 + i * kWarps * split, p.T - 1);
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(b[i].x), "=f"(b[i].y), "=f"(b[i].z), "=f"(b[i].w)
+                                 : "r"(at + t * kTileN * 4)
+                                 : "memory");
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    a[i].x += b[i].x;
+                    a[i].y += b[i].y;
+                    a[i].z += b[i].z;
+                    a[i].w += b[i].w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int t = t0 + i * kWarps * split;
+                if (t < p.T) {
+                    const float gx = s_gx[t];
+                    const uint32_t lo = pack_bf16x2(a[i].x * (gx * gw[0]), a[i].y * (gx * gw[1]));
+                    const uint32_t hi = pack_bf16x2(a[i].z * (gx * gw[2]), a[i].w * (gx * gw[3]));
+                    if (whole) {
+                        *reinterpret_cast<uint2*>(g.dst + (size_t)t * g.ld + (n - g.col0)) = make_uint2(lo, hi);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + e < p.N)
+                                *output_at(p, n + e, t) = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+                    }
+                }
             }
         }
     }

@@ -24,7 +24,7 @@ namespace quant {
 
 constexpr int kNvfp4 = 0, kMxfp4 = 1;  // enum gdn_quant_format
 constexpr uint32_t kTileBytes = 512;
-constexpr int kUnit = 16;        // elements per thread and step
+constexpr int kUnit = 32;        // elements per thread and step of the quantisation
 constexpr int kMaxGroup = 512;   // threads per row
 
 __host__ __device__ constexpr int block_of(int fmt) { return fmt == kNvfp4 ? 16 : 32; }
@@ -92,31 +92,30 @@ __device__ __forceinline__ float row_scale_of(uint32_t row_max) {
     return pow2f(max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100));
 }
 
-// The 16 codes of one thread's unit and its block's scale byte, from the unit, the block's and the
-// row's largest magnitudes.
+// 1 / row scale (nvfp4), from the row's largest magnitude.
+__device__ __forceinline__ float inv_row_scale(uint32_t row_max) {
+    return pow2f(-max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100));
+}
+
+// A block's scale byte from its largest magnitude, and what its elements are multiplied by: 1 / (s g).
 template <int FMT>
-__device__ __forceinline__ void quantize_unit(const uint4& a, const uint4& b, uint32_t block_max, uint32_t row_max,
-                                              uint2& codes, uint32_t& scale) {
-    const bool finite = row_max < 0x7f80u;
-    float inv;  // 1 / (s g)
+__device__ __forceinline__ float block_scale(uint32_t block_max, float inv_g, uint32_t& byte) {
     if constexpr (FMT == kNvfp4) {
-        const int j = max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100);
-        const float inv_g = pow2f(-j);
-        scale = e4m3_bits(snap16(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g * (1.0f / 6.0f)));
-        const float s = e4m3_value(scale);
+        byte = e4m3_bits(snap16(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g * (1.0f / 6.0f)));
+        const float s = e4m3_value(byte);
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-        inv = s > 0.0f ? r * inv_g : 0.0f;
+        return s > 0.0f ? r * inv_g : 0.0f;
     } else {
         const int e = max(static_cast<int>(block_max >> 7) - 127 - 2, -127);
-        scale = static_cast<uint32_t>(e + 127);
-        inv = pow2f(-e);
+        byte = static_cast<uint32_t>(e + 127);
+        return pow2f(-e);
     }
-    if (!finite) {
-        scale = 0;
-        codes = make_uint2(0u, 0u);
-        return;
-    }
+}
+
+// 16 codes of bf16 elements times inv.
+template <int FMT>
+__device__ __forceinline__ uint2 codes16(const uint4& a, const uint4& b, float inv) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float v[16];
 #pragma unroll
@@ -124,12 +123,11 @@ __device__ __forceinline__ void quantize_unit(const uint4& a, const uint4& b, ui
         v[2 * i] = __uint_as_float(w[i] << 16) * inv;
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
     }
-    if constexpr (FMT == kNvfp4) {
+    if constexpr (FMT == kNvfp4) {  // (mxfp4: inv is a power of two, the quotients are exact)
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = snap16(v[i]);
     }
-    codes.x = pack_e2m1x8(v);
-    codes.y = pack_e2m1x8(v + 8);
+    return make_uint2(pack_e2m1x8(v), pack_e2m1x8(v + 8));
 }
 
 struct Params {
@@ -143,89 +141,89 @@ struct Params {
 }  // namespace quant
 
 // One row per group of blockDim.x threads (a multiple of 32), blockDim.y rows per CTA and step; persistent
-// CTAs walk the rows.  A thread takes units of 16 elements, blockDim.x units apart; a row is read once while
-// it fits in kHold units per thread (K <= 16384) and twice above.  The next row's first units are requested
+// CTAs walk the rows.  A thread takes units of 32 elements (two blocks of 16 or one of 32), blockDim.x units
+// apart; a row is read once up to K = 16384 (one unit per thread) and twice above.  The next row is requested
 // before this row's largest magnitude is known, so a row's load latency overlaps the previous row's
-// arithmetic.  kHold is 1 up to K = 8192, else 2 (registers that a short row leaves empty cost occupancy:
-// 16480 x 5120 rows 49 us with 1, 60 us with 2).  Bound: HBM (2 bytes read and about 0.57 written per element).
-template <int FMT, int kHold>
+// arithmetic.  Bound: HBM (2 bytes read and about 0.57 written per element) and, close behind, issue: units
+// of 16 elements, with the row's bookkeeping on half as much data, took 242 instructions each.
+template <int FMT>
 __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const quant::Params p) {
     using namespace quant;
     __shared__ uint32_t s_max[2][kMaxGroup / 32];
     // a projection launched behind this kernel may start its prologue (it waits for this grid's end before
     // it reads what is written here)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int units = p.K / kUnit, step = blockDim.x, lane = threadIdx.x & 31;
+    const int units = p.K / kUnit, step = blockDim.x, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int groups = (p.rows + blockDim.y - 1) / blockDim.y;  // steps of all CTAs
-    uint4 a[kHold], b[kHold];
-    auto load = [&](int g) {
+    const int w = tid >> 5, nw = step >> 5;                     // the row's warps
+    uint4 next[4];
+    auto load = [&](int g, int u, uint4(&x)[4]) {
         const int row = g * blockDim.y + threadIdx.y;
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row * p.K);
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row * p.K) + 4 * u;
+        const bool in = row < p.rows && u < units;
 #pragma unroll
-        for (int h = 0; h < kHold; ++h) {
-            const int u = threadIdx.x + h * step;
-            a[h] = b[h] = make_uint4(0, 0, 0, 0);
-            if (row < p.rows && u < units) {
-                a[h] = __ldg(src + 2 * u);
-                b[h] = __ldg(src + 2 * u + 1);
-            }
-        }
+        for (int i = 0; i < 4; ++i) x[i] = in ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
     };
-    int buf = 0;
-    load(blockIdx.x);
-    for (int g = blockIdx.x; g < groups; g += gridDim.x, buf ^= 1) {
+    load(blockIdx.x, tid, next);
+    for (int g = blockIdx.x, buf = 0; g < groups; g += gridDim.x, buf ^= 1) {
         const int row = g * blockDim.y + threadIdx.y;
         const bool active = row < p.rows;  // (rows do not share a warp)
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(active ? row : 0) * p.K);
-        uint4 ca[kHold], cb[kHold];
-        uint32_t bm[kHold], rm = 0;
-#pragma unroll
-        for (int h = 0; h < kHold; ++h) {
-            ca[h] = a[h];
-            cb[h] = b[h];
-            bm[h] = amax_bits16(ca[h], cb[h]);
-            rm = max(rm, bm[h]);
+        uint4 x[4] = {next[0], next[1], next[2], next[3]};
+        uint32_t m0 = amax_bits16(x[0], x[1]), m1 = amax_bits16(x[2], x[3]);
+        uint32_t rm = max(m0, m1);
+        for (int u = tid + step; u < units; u += step) {
+            uint4 y[4];
+            load(g, u, y);
+            rm = max(rm, max(amax_bits16(y[0], y[1]), amax_bits16(y[2], y[3])));
         }
-        for (int u = threadIdx.x + kHold * step; u < units; u += step)
-            if (active) rm = max(rm, amax_bits16(__ldg(src + 2 * u), __ldg(src + 2 * u + 1)));
-        if (g + gridDim.x < groups) load(g + gridDim.x);
+        if (g + gridDim.x < groups) load(g + gridDim.x, tid, next);
         rm = __reduce_max_sync(0xffffffffu, rm);
-        if (step > 32) {  // the row's warps (blockDim.y rows of step / 32 warps, at most kMaxGroup threads in all)
-            const int w = threadIdx.x >> 5, nw = step >> 5;
+        if (step > 32) {
             if (lane == 0) s_max[buf][threadIdx.y * nw + w] = rm;
             __syncthreads();  // (two buffers: the next row's maxima do not overwrite those still being read)
             rm = __reduce_max_sync(0xffffffffu, s_max[buf][threadIdx.y * nw + (lane < nw ? lane : 0)]);
         }
         if (!active) continue;
-        auto emit = [&](int u, const uint4& ua, const uint4& ub, uint32_t um) {
-            uint2 codes;
-            uint32_t scale;
-            if constexpr (FMT == kMxfp4) um = max(um, __shfl_xor_sync(0xffffffffu, um, 1));  // a block is two units
-            quantize_unit<FMT>(ua, ub, um, rm, codes, scale);
-            if (u < units) *reinterpret_cast<uint2*>(p.codes + (size_t)row * (p.K / 2) + (size_t)u * 8) = codes;
-            // 4 scales of a tile row are one aligned word
-            constexpr int kPer = block_of(FMT) / kUnit;  // units per block
-            uint32_t word = u < units ? scale << (8 * ((lane / kPer) & 3)) : 0u;
-            word = (lane % kPer == 0) ? word : 0u;
-#pragma unroll
-            for (int off = kPer; off < 4 * kPer; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
-            if (lane % (4 * kPer) == 0 && u < units)
-                *reinterpret_cast<uint32_t*>(p.scales + scale_offset(row, u / kPer, p.tiles)) = word;
-        };
-        const int u0 = static_cast<int>(threadIdx.x & ~31u);
-#pragma unroll
-        for (int h = 0; h < kHold; ++h)
-            if (u0 + h * step < units) emit(threadIdx.x + h * step, ca[h], cb[h], bm[h]);
-        for (int v0 = u0 + kHold * step; v0 < units; v0 += step) {
-            const int u = v0 + lane;
-            uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-            if (u < units) {
-                ua = __ldg(src + 2 * u);
-                ub = __ldg(src + 2 * u + 1);
+        const bool finite = rm < 0x7f80u;
+        const float inv_g = FMT == kNvfp4 ? inv_row_scale(rm) : 1.0f;
+        uint8_t* codes = p.codes + (size_t)row * (p.K / 2);
+        uint8_t* scales = p.scales + scale_offset(row, 0, p.tiles);
+        auto emit = [&](int u) {
+            uint32_t b0, b1, word;
+            float i0, i1;
+            if constexpr (FMT == kNvfp4) {
+                i0 = block_scale<FMT>(m0, inv_g, b0);
+                i1 = block_scale<FMT>(m1, inv_g, b1);
+                word = b0 | (b1 << 8);
+            } else {
+                i0 = i1 = block_scale<FMT>(max(m0, m1), 1.0f, b0);
+                word = b0;
             }
-            emit(u, ua, ub, amax_bits16(ua, ub));
+            uint2 lo = codes16<FMT>(x[0], x[1], i0), hi = codes16<FMT>(x[2], x[3], i1);
+            if (!finite) lo = hi = make_uint2(0u, 0u), word = 0u;
+            // 4 scales of a tile row are one aligned word: of 2 lanes, or of 4 (past the row: zeros)
+            if (u >= units) word = 0u;
+            if constexpr (FMT == kNvfp4) {
+                word |= __shfl_down_sync(0xffffffffu, word, 1) << 16;
+            } else {
+                word |= __shfl_down_sync(0xffffffffu, word, 1) << 8;
+                word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
+            }
+            constexpr int kLanes = FMT == kNvfp4 ? 2 : 4;
+            if (u < units) {
+                *reinterpret_cast<uint4*>(codes + 16 * u) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                if ((lane & (kLanes - 1)) == 0)
+                    *reinterpret_cast<uint32_t*>(scales + (u / kLanes) * kTileBytes) = word;
+            }
+        };
+        if (32 * w < units) emit(tid);
+        for (int u0 = 32 * w + step; u0 < units; u0 += step) {  // (whole warps)
+            load(g, u0 + lane, x);
+            m0 = amax_bits16(x[0], x[1]);
+            m1 = amax_bits16(x[2], x[3]);
+            emit(u0 + lane);
         }
-        if (threadIdx.x == 0) p.row_scale[row] = row_scale_of<FMT>(rm);
+        if (tid == 0) p.row_scale[row] = row_scale_of<FMT>(rm);
     }
 }
 
@@ -236,7 +234,7 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
     gdn_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int rows, int K, int tiles,
                           uint16_t* out) {
     using namespace quant;
-    const int units = K / kUnit;
+    const int units = K / 16;
     for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < rows; row += (int64_t)gridDim.x * blockDim.y) {
         const float g = __ldg(row_scale + row);
         const uint2* src = reinterpret_cast<const uint2*>(codes + (size_t)row * (K / 2));
