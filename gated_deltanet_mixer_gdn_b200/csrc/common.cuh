@@ -216,6 +216,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     return true;
 }
 
+// Programmatic launch: a kernel launched so may start before the stream's previous kernel has ended; grid_wait
+// returns when that one has ended and its writes are visible (at once where the launch was an ordinary one).
+// launch_dependents lets a kernel launched so behind this one start once every CTA has called it or ended; called
+// after grid_wait, the dependent sees the effects of everything before this kernel from its start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Make generic-proxy writes to shared memory visible to the async proxy
 // (tensor-core operand reads, TMA).
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(32) gdn_pool_kernel(const __grid_constant__ po
     for (uint32_t i = lane; i < kZeroBytes / 16; i += 32) reinterpret_cast<uint4*>(zero)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
+    grid_wait();
 
     // task -> its set, the pool, the range of the row
     struct Task {

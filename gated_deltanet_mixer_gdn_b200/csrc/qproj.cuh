@@ -96,10 +96,6 @@ __device__ __forceinline__ uint16_t* output_at(const Params& p, int n, int t) {
 
 constexpr uint32_t S_BYTES = 4 * quant::kTileBytes;  // scales of 128 rows and a stage, at most
 
-// The projections are launched while the call's quantisation still runs (programmatic launch); before anything
-// it wrote is read they wait for its end.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ---------------------------------------------------------------- few tokens: the weights' rows as lanes
 namespace few {
 constexpr int kTileN = 128;                           // features per tile (rows of the A operand)
@@ -275,6 +271,7 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
                       scale_bytes(ks), &full[s]);
         };
         const int head = min(C::kStages, ksteps);
+        if (kFuse) grid_wait();
         if (elect_one())
             for (int ks = 0; ks < head; ++ks) load_w(ks, ks);
         __syncwarp();
@@ -334,12 +331,12 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
             if (++s == C::kStages) s = 0, ph ^= 1;
         }
     } else {
+        grid_wait();
         if constexpr (kFuse) quantize_tokens<FMT, C>(p, smem + C::OFF_X, s_amax, rows_ready, tid - 64, k0, ksteps);
         // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
         float* part = reinterpret_cast<float*>(smem);
         if constexpr (!kFuse) {
-            grid_wait();
             if (tid - 64 < p.T) s_gx[tid - 64] = __ldg(p.gx + tid - 64);  // (T <= BN <= 128 threads)
         }
         wait1(done, 0, kErrTimeoutMma);

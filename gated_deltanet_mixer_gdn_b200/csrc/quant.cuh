@@ -150,9 +150,8 @@ template <int FMT>
 __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const quant::Params p) {
     using namespace quant;
     __shared__ uint32_t s_max[2][kMaxGroup / 32];
-    // a projection launched behind this kernel may start its prologue (it waits for this grid's end before
-    // it reads what is written here)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();
+    launch_dependents();  // a projection behind this kernel may start its prologue and load its weights
     const int units = p.K / kUnit, step = blockDim.x, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int groups = (p.rows + blockDim.y - 1) / blockDim.y;  // steps of all CTAs
     const int w = tid >> 5, nw = step >> 5;                     // the row's warps
@@ -234,6 +233,7 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
     gdn_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int rows, int K, int tiles,
                           uint16_t* out) {
     using namespace quant;
+    grid_wait();
     const int units = K / 16;
     for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < rows; row += (int64_t)gridDim.x * blockDim.y) {
         const float g = __ldg(row_scale + row);
