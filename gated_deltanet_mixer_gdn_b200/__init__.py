@@ -740,7 +740,11 @@ def compact_slots(live, state_pool, conv_pool, *, clear: bool = False, dims: Dim
     the live count stay, those behind it fill the free rows before it in ascending order.  ``clear``
     zeroes the rows behind.  Returns the new row of each old row, int32 on the host, -1 where not live."""
     dev, P = _pool_checked(state_pool, conv_pool, dims, "compact_slots")
-    flags = bytes(map(bool, live.tolist() if isinstance(live, torch.Tensor) else live))
+    if isinstance(live, torch.Tensor):
+        if live.dim() != 1:
+            raise ValueError("compact_slots: one flag per pool row")
+        live = live.tolist()
+    flags = bytes(map(bool, live))
     if len(flags) != P:
         raise ValueError("compact_slots: one flag per pool row")
     remap = torch.empty((P,), dtype=torch.int32)

@@ -36,6 +36,14 @@ __host__ __device__ __forceinline__ size_t scale_offset(size_t r, int b, int til
     return ((r >> 7) * tiles + (b >> 2)) * kTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
+// 32 bytes to a 32-byte boundary: one sector per lane (stored as two halves, 32 bytes apart between lanes, each
+// sector goes to L2 twice: 16480 x 5120 values 41 us against 38).
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // 8 floats -> 8 E2M1 codes (round to nearest even, saturating), element i in nibble i.
@@ -235,6 +243,7 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
     using namespace quant;
     grid_wait();
     const int units = K / 16;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;  // (rows are multiples of 128 bytes)
     for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < rows; row += (int64_t)gridDim.x * blockDim.y) {
         const float g = __ldg(row_scale + row);
         const uint2* src = reinterpret_cast<const uint2*>(codes + (size_t)row * (K / 2));
@@ -257,8 +266,13 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
                 const __half2 h2 = *reinterpret_cast<__half2*>(&h);
                 o[j] = pack_bf16x2(__low2float(h2) * s, __high2float(h2) * s);
             }
-            dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            if (wide) {
+                store32(dst + 2 * u, lo, hi);
+            } else {
+                dst[2 * u] = lo;
+                dst[2 * u + 1] = hi;
+            }
         }
     }
 }

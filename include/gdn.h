@@ -304,7 +304,8 @@ int gdn_out_proj(const gdn_dims* dims, int32_t T, int32_t hidden, const uint16_t
  *     and saturated; row_scale[r] = 1.
  * A row that holds an infinity or a NaN gets row_scale NaN: all its values are
  * NaN, other rows are not affected.  Weights quantised elsewhere fit in when
- * laid out so, with any finite row scales (a tensor-wide scale repeated).
+ * laid out so, with any finite row scales (a tensor-wide scale repeated) and
+ * E4M3 scales without a sign.
  *   codes     uint8 [rows][K/2], element 2i in the low nibble of byte i
  *   scales    uint8, gdn_quant_scale_bytes(format, rows, K) bytes: tiles of
  *             128 rows x 4 blocks of 512 bytes, tiles of a row block next to
@@ -313,9 +314,10 @@ int gdn_out_proj(const gdn_dims* dims, int32_t T, int32_t hidden, const uint16_t
  *             last in its tile are neither written nor used.
  *   row_scale f32 [rows]
  * K is a multiple of 64 (GDN_ERR_UNSUPPORTED otherwise), codes, scales, x and
- * out 16-byte aligned.  rows = 0 is a legal no-op.  The value is exact in bf16
- * unless it leaves bf16's range: gdn_dequantize(gdn_quantize(x)) returns the
- * rounded values without a further rounding.
+ * out 16-byte aligned.  rows = 0 is a legal no-op.  With row scales that are
+ * powers of two the value is exact in bf16 unless it leaves bf16's range:
+ * gdn_dequantize(gdn_quantize(x)) returns the rounded values without a further
+ * rounding.
  */
 enum gdn_quant_format { GDN_NVFP4 = 0, GDN_MXFP4 = 1 };
 size_t gdn_quant_scale_bytes(int32_t format, int32_t rows, int32_t K);

@@ -173,5 +173,7 @@ def test_refusals(dev):
         gdn.copy_slots([0], [1], st, cv)  # the pools of other dims
     with pytest.raises(ValueError):
         gdn.compact_slots([True] * 3, st, cv, dims=SMALL)
+    with pytest.raises(ValueError):
+        gdn.compact_slots(torch.ones((4, 1)), st, cv, dims=SMALL)
     torch.cuda.synchronize(dev)
     assert _same(st, before[0]) and _same(cv, before[1])

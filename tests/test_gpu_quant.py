@@ -30,7 +30,7 @@ def _check(x, fmt, dev):
     assert np.array_equal(got[1], sc)
     assert np.array_equal(got[0], codes)
     want = ref.values(codes, sc, row, fmt)
-    want = np.where(np.abs(want) >= 2.0 ** 128, np.sign(want) * np.inf, want)
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
     assert np.array_equal(back.double().cpu().numpy(), want, equal_nan=True)
 
 
