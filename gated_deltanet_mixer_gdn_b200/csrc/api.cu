@@ -1381,13 +1381,27 @@ int qproj_pairs(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, in
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, mSw, mSx, p));
 }
 
-// Clusters that share a tile's K while the tiles leave SMs idle, at least two stages each.
-int few_split(const qproj::Params& p, int nsm) {
-    const int tiles = (p.N + qproj::few::kTileN - 1) / qproj::few::kTileN, steps = (p.K + qproj::BK - 1) / qproj::BK;
-    int split = nsm / tiles;
-    if (split > steps / 2) split = steps / 2;
-    if (split > qproj::few::kMaxSplit) split = qproj::few::kMaxSplit;
-    return split < 1 ? 1 : split;
+// Clusters of `cfg`'s size that the current device runs at once (0: unknown); asked once per kernel, device and
+// size while the table has room.
+int resident_clusters(const void* kernel, int size, const cudaLaunchConfig_t& cfg) {
+    struct Known {
+        const void* kernel;
+        int dev, size, clusters;
+    };
+    static std::mutex mu;
+    static Known known[256];
+    static int count = 0;
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < count; ++i)
+        if (known[i].kernel == kernel && known[i].dev == dev && known[i].size == size) return known[i].clusters;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // (not the launch's error)
+        n = 0;
+    }
+    if (count < 256) known[count++] = Known{kernel, dev, size, n};
+    return n;
 }
 
 template <int FMT, int BN, bool kFuse>
@@ -1400,15 +1414,24 @@ int qproj_few(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, int 
     auto kernel = gdn_qproj_few_kernel<FMT, BN, kFuse>;
     const int st = smem_optin(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES);
     if (st != GDN_OK) return st;
-    const int split = few_split(p, nsm);
+    // Clusters that share a tile's K while the tiles leave SMs idle, at least two stages per CTA, and only as large as
+    // lets all of them run at once: a cluster lies inside one group of SMs, so 37 tiles by 4 take two rounds (12.3 us)
+    // where 37 by 3 take one (8.3 us).
+    const int tiles = (p.N + qproj::few::kTileN - 1) / qproj::few::kTileN, steps = (p.K + qproj::BK - 1) / qproj::BK;
+    int split = nsm / tiles;
+    if (split > steps / 2) split = steps / 2;
+    if (split > qproj::few::kMaxSplit) split = qproj::few::kMaxSplit;
     cudaLaunchAttribute attr[2];
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 1;
     attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = split;
-    const cudaLaunchConfig_t cfg = early_launch(dim3((p.N + qproj::few::kTileN - 1) / qproj::few::kTileN, 1, split), C::kThreads,
-                                            C::SMEM_BYTES, stream, attr, split > 1 ? 2 : 1);
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, p));
+    for (;; --split) {
+        if (split < 1) split = 1;
+        attr[1].val.clusterDim.z = split;
+        const cudaLaunchConfig_t cfg = early_launch(dim3(tiles, 1, split), C::kThreads, C::SMEM_BYTES, stream, attr, split > 1 ? 2 : 1);
+        if (split > 1 && resident_clusters(reinterpret_cast<const void*>(kernel), split, cfg) < tiles) continue;
+        return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mW, mX, p));
+    }
 }
 
 template <int FMT>

@@ -71,7 +71,8 @@ def test_in_proj(dev, fmt, T, hidden, kh, vh):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,hidden,vh", [(1, 64, 1), (3, 5120, 1), (8, 192, 48), (31, 1024, 12), (64, 320, 9),
                                          (100, 64, 3), (130, 448, 8), (600, 1088, 5), (1, 1, 2), (40, 37, 3),
-                                         (300, 259, 4)])
+                                         (300, 259, 4), (9, 2304, 48), (9, 2688, 48), (40, 2944, 48), (2, 3200, 48),
+                                         (17, 3584, 48), (9, 4736, 48), (5, 128, 48), (1, 1000, 48)])
 def test_out_proj(dev, fmt, T, hidden, vh):
     dims = Dims(num_k_heads=1 if vh < 9 else 3 if vh < 12 else vh // 3, num_v_heads=vh)
     K = dims.value_width
@@ -82,7 +83,7 @@ def test_out_proj(dev, fmt, T, hidden, vh):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T", [1, 64, 600, 8192])
+@pytest.mark.parametrize("T", [1, 64, 100, 600, 8192])
 def test_layer_shape_sampled(dev, fmt, T):
     """The 27B layer's in_proj (16480 x 5120) and out_proj (5120 x 6144) on sampled tokens and features."""
     dims, hidden = gdn.MODEL, 5120
