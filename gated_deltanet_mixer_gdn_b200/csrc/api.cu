@@ -1496,14 +1496,18 @@ int proj_quant(int format, int32_t T, int32_t K, int32_t N, const uint16_t* x, c
     p.gw = w_row_scale;
     p.nseg = nseg;
     for (int i = 0; i < nseg; ++i) p.seg[i] = seg[i];
-    if (few_fuse(T, K))
-        return format == GDN_NVFP4 ? qproj_few<quant::kNvfp4, 16, true>(nullptr, w_codes, p, nsm, s)
-                                   : qproj_few<quant::kMxfp4, 16, true>(nullptr, w_codes, p, nsm, s);
-    if ((st = quantize_launch(format, T, K, x, wsb, wsb + q.off_scales,
-                              reinterpret_cast<float*>(wsb + q.off_row_scale), s)) != GDN_OK)
-        return st;
-    return format == GDN_NVFP4 ? qproj_launch<quant::kNvfp4>(wsb, w_codes, p, nsm, s)
-                                    : qproj_launch<quant::kMxfp4>(wsb, w_codes, p, nsm, s);
+    try {
+        if (few_fuse(T, K))
+            return format == GDN_NVFP4 ? qproj_few<quant::kNvfp4, 16, true>(nullptr, w_codes, p, nsm, s)
+                                       : qproj_few<quant::kMxfp4, 16, true>(nullptr, w_codes, p, nsm, s);
+        if ((st = quantize_launch(format, T, K, x, wsb, wsb + q.off_scales,
+                                  reinterpret_cast<float*>(wsb + q.off_row_scale), s)) != GDN_OK)
+            return st;
+        return format == GDN_NVFP4 ? qproj_launch<quant::kNvfp4>(wsb, w_codes, p, nsm, s)
+                                   : qproj_launch<quant::kMxfp4>(wsb, w_codes, p, nsm, s);
+    } catch (const std::bad_alloc&) {  // (the list of kernels whose shared memory has been opted in)
+        return GDN_ERR_HOST_MEMORY;
+    }
 }
 
 // ---------------------------------------------------------------- pool rows
