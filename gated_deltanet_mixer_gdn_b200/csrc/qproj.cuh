@@ -114,7 +114,7 @@ struct Cfg {
     static constexpr uint32_t OFF_X = kStages * STAGE_BYTES;  // (kFuse) all stages' tokens
     static constexpr uint32_t OFF_MISC = OFF_X + (kFuse ? kMaxSteps * X_STAGE : 0);
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 256 + BN * 4 + 1024;
-    static constexpr int kThreads = 64 + (kFuse ? kRowThreads : 128);  // warp 0 loads, warp 1 products, rows and sums
+    static constexpr int kThreads = 64 + (kFuse ? kRowThreads : 256);  // warp 0 loads, warp 1 products, rows and sums
     // tensor memory: the sums (BN columns), then per stage 16 columns of weight scales and 16 of token
     // scales; a stage's columns are free when its shared memory is
     static constexpr uint32_t TMEM_COLS = 512;
@@ -374,12 +374,14 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
                 if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(r));
                 float4 b[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {  // (past the last token: the last token's, not stored)
-                    const int t = min(t0 + i * kWarps * split, p.T - 1);
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(b[i].x), "=f"(b[i].y), "=f"(b[i].z), "=f"(b[i].w)
-                                 : "r"(at + t * kTileN * 4)
-                                 : "memory");
+                for (int i = 0; i < kBatch; ++i) {
+                    b[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    const int t = t0 + i * kWarps * split;
+                    if (t < p.T)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(b[i].x), "=f"(b[i].y), "=f"(b[i].z), "=f"(b[i].w)
+                                     : "r"(at + t * kTileN * 4)
+                                     : "memory");
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
