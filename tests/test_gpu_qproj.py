@@ -83,7 +83,7 @@ def test_out_proj(dev, fmt, T, hidden, vh):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T", [1, 64, 100, 600, 8192])
+@pytest.mark.parametrize("T", [1, 64, 100, 600, 8192, 8500])
 def test_layer_shape_sampled(dev, fmt, T):
     """The 27B layer's in_proj (16480 x 5120) and out_proj (5120 x 6144) on sampled tokens and features."""
     dims, hidden = gdn.MODEL, 5120
