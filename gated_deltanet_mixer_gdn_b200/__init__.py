@@ -553,9 +553,9 @@ def quantize(x, format: str = "nvfp4", *, out: Optional[QuantTensor] = None) -> 
         raise ValueError("quantize: K must be a multiple of 64")
     if out is None:
         out = object.__new__(QuantTensor)  # (made here: nothing to check)
-        out.__dict__.update(codes=x.new_empty((rows, K // 2), dtype=torch.uint8),
-                            scales=x.new_empty(_scale_shape(format, rows, K), dtype=torch.uint8),
-                            row_scale=x.new_empty((rows,), dtype=torch.float32), format=format)
+        out.__dict__.update(codes=x.new_empty(rows, K // 2, dtype=torch.uint8),
+                            scales=x.new_empty(*_scale_shape(format, rows, K), dtype=torch.uint8),
+                            row_scale=x.new_empty(rows, dtype=torch.float32), format=format)
     fmt, orows, oK, ptrs = _quant_checked(out, "out", dev)
     if out.format != format or (orows, oK) != (rows, K):
         raise ValueError("quantize: out has another format or shape")
@@ -570,7 +570,7 @@ def dequantize(q: QuantTensor, *, out=None):
     dev = _device_of(q.codes)
     fmt, rows, K, ptrs = _quant_checked(q, "q", dev)
     if out is None:
-        out = q.codes.new_empty((rows, K), dtype=torch.bfloat16)
+        out = q.codes.new_empty(rows, K, dtype=torch.bfloat16)
     else:
         _need(out, torch.bfloat16, "out", dev)
         if tuple(out.shape) != (rows, K):
@@ -581,7 +581,7 @@ def dequantize(q: QuantTensor, *, out=None):
 
 def _proj_out(out, x, T: int, widths, what: str):
     if out is None:
-        return [x.new_empty((T, w)) for w in widths]
+        return [x.new_empty(T, w) for w in widths]
     for t, w in zip(out, widths):
         _need(t, torch.bfloat16, f"{what} out", x.device)
         if tuple(t.shape) != (T, w):
@@ -603,7 +603,7 @@ def in_proj_quant(x, w_in: QuantTensor, *, dims: Dims = MODEL, out=None):
     L = load_library()
     qkv, z, a, b = _proj_out(out, x, T, (C, VD, Vh, Vh), "in_proj_quant")
     ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
-    ws = x.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
+    ws = x.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _check(_on(dev, L.gdn_in_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, K, x.data_ptr(), *ptrs, qkv.data_ptr(),
                z.data_ptr(), b.data_ptr(), a.data_ptr(), _ptr(ws), ws_bytes), "gdn_in_proj_quant")
     return qkv, z, a, b
@@ -621,7 +621,7 @@ def out_proj_quant(y, w_out: QuantTensor, *, dims: Dims = MODEL, out=None):
     L = load_library()
     out, = _proj_out(None if out is None else [out], y, T, (hidden,), "out_proj_quant")
     ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
-    ws = y.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
+    ws = y.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _check(_on(dev, L.gdn_out_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, hidden, y.data_ptr(), *ptrs,
                out.data_ptr(), _ptr(ws), ws_bytes), "gdn_out_proj_quant")
     return out
