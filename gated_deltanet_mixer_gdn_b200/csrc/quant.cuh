@@ -85,11 +85,12 @@ __device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) 
     return max(r & 0xffffu, r >> 16);
 }
 
-// v rounded to 16 significant bits.  A quotient formed with a rounded reciprocal may miss an exact tie by a
-// relative 2^-22; the quotients taken here (8 bits over at most 4) are ties of the format rounded to next
-// or at least a relative 1/255 away from one, so this restores the former and keeps the latter apart (and
-// keeps the sign of a zero).
-__device__ __forceinline__ float snap16(float v) { return __uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u); }
+// A quotient formed with a rounded reciprocal may miss an exact tie by a relative 2^-21.  The quotients taken here
+// (8 bits over at most 4) are ties of the format rounded to next, or at least a relative 1/255 away from one: taken
+// kAbove times too large (2^-17), and their last 8 bits dropped, ties come out exact, the others stay on their side,
+// and a zero keeps its sign.
+constexpr float kAbove = 0x1.00008p0f;
+__device__ __forceinline__ float snap16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffff00u); }
 
 // A row's scale from its largest magnitude (bf16 bits).
 template <int FMT>
@@ -105,15 +106,16 @@ __device__ __forceinline__ float inv_row_scale(uint32_t row_max) {
     return pow2f(-max(static_cast<int>(row_max >> 7) - 127 - 11 + ((row_max & 127u) > 40u ? 1 : 0), -100));
 }
 
-// A block's scale byte from its largest magnitude, and what its elements are multiplied by: 1 / (s g).
+// A block's scale byte from its largest magnitude, and what its elements are multiplied by: 1 / (s g) (nvfp4:
+// kAbove times that, for snap16).
 template <int FMT>
 __device__ __forceinline__ float block_scale(uint32_t block_max, float inv_g, uint32_t& byte) {
     if constexpr (FMT == kNvfp4) {
-        byte = e4m3_bits(snap16(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g * (1.0f / 6.0f)));
+        byte = e4m3_bits(snap16(bf16_bits_to_float(static_cast<uint16_t>(block_max)) * inv_g * (kAbove / 6.0f)));
         const float s = e4m3_value(byte);
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-        return s > 0.0f ? r * inv_g : 0.0f;
+        return s > 0.0f ? r * inv_g * kAbove : 0.0f;
     } else {
         const int e = max(static_cast<int>(block_max >> 7) - 127 - 2, -127);
         byte = static_cast<uint32_t>(e + 127);
