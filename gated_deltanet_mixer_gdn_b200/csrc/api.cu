@@ -1266,7 +1266,7 @@ const char* gdn_status_string(int status) {
     }
 }
 
-int gdn_version(void) { return 100; }
+int gdn_version(void) { return 200; }
 
 }  // extern "C"
 

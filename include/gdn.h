@@ -26,11 +26,11 @@
  * Memory: every pointer is DEVICE memory owned by the caller, 16-byte
  * aligned, densely packed in the layouts given.  bf16 tensors are passed as
  * uint16_t bit patterns.  The library allocates no device memory and keeps no
- * state between calls other than a per-process cache of driver entry points,
- * two internal streams and a few events per device (created by the first
- * prefill that overlaps its kernels, see gdn_prefill), a device-side error word
- * with the decode kernels' wait bound, and the fixed scratch array of
- * gdn_prefill_noalloc.
+ * state between calls other than per-process caches of driver entry points and
+ * kernel attributes, two internal streams and a few events per device (created
+ * by the first prefill that overlaps its kernels, see gdn_prefill), a
+ * device-side error word with the decode kernels' wait bound, and the fixed
+ * scratch array of gdn_prefill_noalloc.
  *
  * Streams: `stream` is a cudaStream_t (NULL = the legacy default stream).
  * Every call only enqueues work on it and returns; results are ready when
