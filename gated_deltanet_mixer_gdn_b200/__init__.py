@@ -64,6 +64,8 @@ _lock = threading.Lock()
 def load_library() -> ctypes.CDLL:
     """Load libgdn_b200.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -186,7 +188,15 @@ def _device_of(qkv: torch.Tensor) -> torch.device:
     return qkv.device
 
 
-_dims_of = functools.lru_cache(maxsize=64)(_dims_c)  # (the struct is only read)
+@functools.lru_cache(maxsize=64)
+def _dims_ref(dims: Dims):
+    """A reference to the C struct of `dims` (only ever read)."""
+    return ctypes.byref(_dims_c(dims))
+
+
+@functools.lru_cache(maxsize=1024)
+def _proj_workspace(fmt: int, T: int, K: int) -> int:
+    return load_library().gdn_proj_quant_workspace_size(fmt, T, K)
 
 
 # the current stream of a device by its index (3 us of the small calls went into torch.cuda.current_stream)
@@ -579,11 +589,12 @@ def dequantize(q: QuantTensor, *, out=None):
     return out
 
 
-def _proj_out(out, x, T: int, widths, what: str):
-    if out is None:
-        return [x.new_empty(T, w) for w in widths]
+def _proj_out(out, T: int, widths, dev: torch.device, what: str):
+    out = list(out)
+    if len(out) != len(widths):
+        raise ValueError(f"{what}: {len(widths)} outputs")
     for t, w in zip(out, widths):
-        _need(t, torch.bfloat16, f"{what} out", x.device)
+        _need(t, torch.bfloat16, f"{what} out", dev)
         if tuple(t.shape) != (T, w):
             raise ValueError(f"{what}: out shape")
     return out
@@ -601,10 +612,13 @@ def in_proj_quant(x, w_in: QuantTensor, *, dims: Dims = MODEL, out=None):
         raise ValueError("in_proj_quant: shape mismatch")
     T = x.shape[0]
     L = load_library()
-    qkv, z, a, b = _proj_out(out, x, T, (C, VD, Vh, Vh), "in_proj_quant")
-    ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
+    if out is None:
+        qkv, z, a, b = x.new_empty(T, C), x.new_empty(T, VD), x.new_empty(T, Vh), x.new_empty(T, Vh)
+    else:
+        qkv, z, a, b = _proj_out(out, T, (C, VD, Vh, Vh), dev, "in_proj_quant")
+    ws_bytes = _proj_workspace(fmt, T, K)
     ws = x.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
-    _check(_on(dev, L.gdn_in_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, K, x.data_ptr(), *ptrs, qkv.data_ptr(),
+    _check(_on(dev, L.gdn_in_proj_quant, _dims_ref(dims), fmt, T, K, x.data_ptr(), *ptrs, qkv.data_ptr(),
                z.data_ptr(), b.data_ptr(), a.data_ptr(), _ptr(ws), ws_bytes), "gdn_in_proj_quant")
     return qkv, z, a, b
 
@@ -619,10 +633,10 @@ def out_proj_quant(y, w_out: QuantTensor, *, dims: Dims = MODEL, out=None):
         raise ValueError("out_proj_quant: shape mismatch")
     T = y.shape[0]
     L = load_library()
-    out, = _proj_out(None if out is None else [out], y, T, (hidden,), "out_proj_quant")
-    ws_bytes = L.gdn_proj_quant_workspace_size(fmt, T, K)
+    out = y.new_empty(T, hidden) if out is None else _proj_out([out], T, (hidden,), dev, "out_proj_quant")[0]
+    ws_bytes = _proj_workspace(fmt, T, K)
     ws = y.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
-    _check(_on(dev, L.gdn_out_proj_quant, ctypes.byref(_dims_of(dims)), fmt, T, hidden, y.data_ptr(), *ptrs,
+    _check(_on(dev, L.gdn_out_proj_quant, _dims_ref(dims), fmt, T, hidden, y.data_ptr(), *ptrs,
                out.data_ptr(), _ptr(ws), ws_bytes), "gdn_out_proj_quant")
     return out
 
@@ -725,7 +739,7 @@ def copy_slots(src, dst, state_pool, conv_pool, *, dims: Dims = MODEL):
     (s, n), (d, m) = _host_table(src), _host_table(dst)
     if n != m:
         raise ValueError("copy_slots: one source per destination")
-    _check(_on(dev, load_library().gdn_copy_slots, ctypes.byref(_dims_of(dims)), n, s.buffer_info()[0],
+    _check(_on(dev, load_library().gdn_copy_slots, _dims_ref(dims), n, s.buffer_info()[0],
                d.buffer_info()[0], P, state_pool.data_ptr(), conv_pool.data_ptr()), "gdn_copy_slots")
 
 
@@ -748,7 +762,7 @@ def compact_slots(live, state_pool, conv_pool, *, clear: bool = False, dims: Dim
     if len(flags) != P:
         raise ValueError("compact_slots: one flag per pool row")
     remap = torch.empty((P,), dtype=torch.int32)
-    _check(_on(dev, load_library().gdn_compact_slots, ctypes.byref(_dims_of(dims)), P, flags, bool(clear),
+    _check(_on(dev, load_library().gdn_compact_slots, _dims_ref(dims), P, flags, bool(clear),
                state_pool.data_ptr(), conv_pool.data_ptr(), remap.data_ptr()), "gdn_compact_slots")
     return remap
 
