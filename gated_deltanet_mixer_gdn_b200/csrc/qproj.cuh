@@ -94,6 +94,34 @@ __device__ __forceinline__ uint16_t* output_at(const Params& p, int n, int t) {
     return g.dst + (size_t)t * g.ld + (n - g.col0);
 }
 
+// Sums times the row scales: a token's gx is a power of two in [2^-100, 2^117], 1, or NaN, a feature's gw any finite
+// number.  Their product may leave f32's range where v gx gw does not (2^114 2^15 over a sum that cancels, 2^-100
+// 2^-50 under a large one), so a sum v (in nvfp4 0 or 2^-20 <= |v| <= 2^40) is scaled as ((v x) gw) y with gx = x y:
+// up to gx = 2^+-79 v gx is in range, and y = 1; beyond, half of gx's exponent comes before gw and half after it, so
+// that nothing overflows unless the result does, and nothing is lost that it still shows.  The factors x and y are
+// exact: the result has gw's one rounding.
+__device__ __forceinline__ float2 split_scale(float gx) {
+    const int e = static_cast<int>(__float_as_uint(gx) >> 23) - 127;
+    if ((e > -80 && e < 80) || e == 128) return make_float2(gx, 1.0f);
+    return make_float2(quant::pow2f(e >> 1), quant::pow2f(e - (e >> 1)));
+}
+
+// Two products in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+// Two sums of a token times the row scales, as a bf16 pair.
+__device__ __forceinline__ uint32_t scale_pack2(float v0, float v1, float2 gx, float gw0, float gw1) {
+    const float2 r = mul2(mul2(mul2(make_float2(v0, v1), make_float2(gx.x, gx.x)), make_float2(gw0, gw1)),
+                          make_float2(gx.y, gx.y));
+    return pack_bf16x2(r.x, r.y);
+}
+
 constexpr uint32_t S_BYTES = 4 * quant::kTileBytes;  // scales of 128 rows and a stage, at most
 
 // ---------------------------------------------------------------- few tokens: the weights' rows as lanes
@@ -113,7 +141,8 @@ struct Cfg {
     static constexpr int kStages = kFuse ? 7 : 6;  // (more: 64 tokens 16.5 us with 7 against 16.1, 32 tokens 14.5 with 9 against 13.9)
     static constexpr uint32_t OFF_X = kStages * STAGE_BYTES;  // (kFuse) all stages' tokens
     static constexpr uint32_t OFF_MISC = OFF_X + (kFuse ? kMaxSteps * X_STAGE : 0);
-    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 256 + BN * 4 + 1024;
+    static constexpr uint32_t OFF_AMAX = OFF_MISC + 256 + BN * 8;  // (kFuse) behind the row scales
+    static constexpr uint32_t SMEM_BYTES = OFF_AMAX + (kFuse ? BN * 4 : 0) + 1024;
     static constexpr int kThreads = 64 + (kFuse ? kRowThreads : 256);  // warp 0 loads, warp 1 products, rows and sums
     // tensor memory: the sums (BN columns), then per stage 16 columns of weight scales and 16 of token
     // scales; a stage's columns are free when its shared memory is
@@ -128,9 +157,9 @@ struct Cfg {
 
 // (kFuse) The tokens' rows, held in registers by kRowThreads threads: row maxima, then the codes (swizzled
 // rows of 128 bytes per stage) and scale tiles of stages [k0, k0 + ksteps) into shared memory at `out`, and
-// the row scales over the maxima.  The same values as gdn_quantize_kernel's.
+// the split row scales.  The same values as gdn_quantize_kernel's.
 template <int FMT, class C>
-__device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t* out, uint32_t* s_amax,
+__device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t* out, uint32_t* s_amax, float2* s_gx,
                                                 uint64_t* rows_ready, int tid, int k0, int ksteps) {
     using namespace qproj;
     using namespace qproj::few;
@@ -187,8 +216,7 @@ __device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t*
     }
     fence_proxy_async_smem();
     mbar_arrive(rows_ready);
-    named_barrier_sync(1, kRowThreads);  // the maxima have been read
-    if (tid < p.T) s_amax[tid] = __float_as_uint(quant::row_scale_of<FMT>(s_amax[tid]));
+    if (tid < p.T) s_gx[tid] = split_scale(quant::row_scale_of<FMT>(s_amax[tid]));
 }
 
 // At most 128 tokens: a tile is 128 features x all BN (>= T) tokens, the weights the A operand, so that few
@@ -216,8 +244,8 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
     uint64_t* done = empty + C::kStages;
     uint64_t* rows_ready = done + 1;  // (kFuse) the tokens' codes and scales are in shared memory
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 192);
-    float* s_gx = reinterpret_cast<float*>(smem + C::OFF_MISC + 256);          // [BN] the tokens' row scales
-    uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_gx);                      // (kFuse) their maxima before
+    float2* s_gx = reinterpret_cast<float2*>(smem + C::OFF_MISC + 256);        // [BN] the tokens' row scales, split
+    uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);        // (kFuse) the tokens' largest magnitudes
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n0 = blockIdx.x * kTileN;
     const int split = gridDim.z, rank = blockIdx.z;  // (the cluster spans z)
@@ -332,12 +360,12 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         }
     } else {
         grid_wait();
-        if constexpr (kFuse) quantize_tokens<FMT, C>(p, smem + C::OFF_X, s_amax, rows_ready, tid - 64, k0, ksteps);
+        if constexpr (kFuse) quantize_tokens<FMT, C>(p, smem + C::OFF_X, s_amax, s_gx, rows_ready, tid - 64, k0, ksteps);
         // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
         float* part = reinterpret_cast<float*>(smem);
         if constexpr (!kFuse) {
-            if (tid - 64 < p.T) s_gx[tid - 64] = __ldg(p.gx + tid - 64);  // (T <= BN <= 128 threads)
+            if (tid - 64 < p.T) s_gx[tid - 64] = split_scale(__ldg(p.gx + tid - 64));  // (T <= BN <= 128 threads)
         }
         wait1(done, 0, kErrTimeoutMma);
         __syncwarp();
@@ -395,9 +423,9 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
             for (int i = 0; i < kBatch; ++i) {
                 const int t = t0 + i * kWarps * split;
                 if (t < p.T) {
-                    const float gx = s_gx[t];
-                    const uint32_t lo = pack_bf16x2(a[i].x * (gx * gw[0]), a[i].y * (gx * gw[1]));
-                    const uint32_t hi = pack_bf16x2(a[i].z * (gx * gw[2]), a[i].w * (gx * gw[3]));
+                    const float2 gx = s_gx[t];
+                    const uint32_t lo = scale_pack2(a[i].x, a[i].y, gx, gw[0], gw[1]);
+                    const uint32_t hi = scale_pack2(a[i].z, a[i].w, gx, gw[2], gw[3]);
                     if (whole) {
                         *reinterpret_cast<uint2*>(g.dst + (size_t)t * g.ld + (n - g.col0)) = make_uint2(lo, hi);
                     } else {
@@ -482,12 +510,12 @@ __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t
 }
 
 // 32 sums of one token (features c0 ..) times the row scales, as bf16 pairs.
-__device__ __forceinline__ void scale_pack32(const float (&v)[32], float gx, const float* gw, uint32_t (&o)[16]) {
+__device__ __forceinline__ void scale_pack32(const float (&v)[32], float2 gx, const float* gw, uint32_t (&o)[16]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float4 g = reinterpret_cast<const float4*>(gw)[e];
-        o[2 * e] = pack_bf16x2(v[4 * e] * (gx * g.x), v[4 * e + 1] * (gx * g.y));
-        o[2 * e + 1] = pack_bf16x2(v[4 * e + 2] * (gx * g.z), v[4 * e + 3] * (gx * g.w));
+        o[2 * e] = scale_pack2(v[4 * e], v[4 * e + 1], gx, g.x, g.y);
+        o[2 * e + 1] = scale_pack2(v[4 * e + 2], v[4 * e + 3], gx, g.z, g.w);
     }
 }
 
@@ -707,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             const int row = tm * kTileM + 128 * rank + 32 * q4 + lane, n0 = tn * kTileN;
             float* gw = s_gw + (it & 1) * kTileN;
             for (int i = et; i < kTileN; i += 256) gw[i] = n0 + i < p.N ? __ldg(p.gw + n0 + i) : 0.0f;
-            const float gx = row < p.T ? __ldg(p.gx + row) : 0.0f;
+            const float2 gx = split_scale(row < p.T ? __ldg(p.gx + row) : 1.0f);
             named_barrier_sync(1, 256);
             wait1(&acc_full[it & 1], (it >> 1) & 1, kErrTimeoutMma);
             __syncwarp();

@@ -331,8 +331,9 @@ int gdn_dequantize(int32_t format, int32_t rows, int32_t K, const uint8_t* codes
  * quantised (codes, scales and row scales of [N][K], N and K as in the bf16
  * projections), the tokens x (y) bf16 [T][K] are quantised row by row in the
  * same format inside the call, each token by itself.  The block-scaled
- * products are summed in f32, multiplied by the product of the two row scales
- * (formed in f32, so it has to lie in f32's range) and rounded once to bf16.  Outputs as for gdn_in_proj / gdn_out_proj, 16-byte aligned.
+ * products are summed in f32, multiplied by the two row scales (in steps that
+ * leave f32's range only where the result does) and rounded once to bf16.
+ * Outputs as for gdn_in_proj / gdn_out_proj, 16-byte aligned.
  * workspace: gdn_proj_quant_workspace_size(format, T, K) bytes (the quantised
  * tokens; 0 for a few tokens, which the projection quantises on chip: NULL is
  * legal then), 16-byte aligned.  K a multiple of 64 (GDN_ERR_UNSUPPORTED
