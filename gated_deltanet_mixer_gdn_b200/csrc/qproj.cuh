@@ -106,15 +106,6 @@ __device__ __forceinline__ float2 split_scale(float gx) {
     return make_float2(quant::pow2f(e >> 1), quant::pow2f(e - (e >> 1)));
 }
 
-// Two products in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
-        "mov.b64 {%0, %1}, x;\n\t}\n"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 // Two sums of a token times the row scales, as a bf16 pair.
 __device__ __forceinline__ uint32_t scale_pack2(float v0, float v1, float2 gx, float gw0, float gw1) {
     const float2 r = mul2(mul2(mul2(make_float2(v0, v1), make_float2(gx.x, gx.x)), make_float2(gw0, gw1)),

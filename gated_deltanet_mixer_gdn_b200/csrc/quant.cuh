@@ -256,7 +256,11 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
             float s;
             if (FMT == kNvfp4) s = e4m3_value(sb);
             else s = sb == 255u ? __uint_as_float(0x7fc00000u) : (sb == 0u ? __uint_as_float(1u << 22) : __uint_as_float(sb << 23));
-            s *= g;
+            // code * (s g); where s g overflows (row scales made elsewhere) (code * s) g: a code of 0 stays 0, and small
+            // codes may have finite values
+            const bool far = fabsf(s * g) > 0x1.fffffep127f;  // (not for a NaN)
+            const float2 f0 = far ? make_float2(s, s) : make_float2(s * g, s * g);
+            const float2 f1 = far ? make_float2(g, g) : make_float2(1.0f, 1.0f);
             uint32_t o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -265,8 +269,8 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
                 asm("{\n\t.reg .b8 b0, b1;\n\tmov.b16 {b0, b1}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}\n"
                     : "=r"(h)
                     : "h"(static_cast<uint16_t>(byte)));
-                const __half2 h2 = *reinterpret_cast<__half2*>(&h);
-                o[j] = pack_bf16x2(__low2float(h2) * s, __high2float(h2) * s);
+                const float2 v = mul2(mul2(__half22float2(*reinterpret_cast<__half2*>(&h)), f0), f1);
+                o[j] = pack_bf16x2(v.x, v.y);
             }
             const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
             if (wide) {
