@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         for (int ks = max(issued - C::kStages, 0); ks < issued; ++ks)
             mbar_wait(&full[ks % C::kStages], (ks / C::kStages) & 1);
     } else if (warp == 1) {
+        grid_wait();  // (a bounded wait starts only when the kernel before this one has ended)
         const uint64_t kDesc = sw128_desc(0, 16, 1024), sDesc = scale_desc(0);
         uint32_t s = 0, ph = 0;
         if (kFuse) wait1(rows_ready, 0, kErrTimeoutTma);
@@ -659,6 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
     } else if (warp == 1) {
         // ---------------- products (rank 0)
         if (rank == 0) {
+            grid_wait();  // (as above: before the first bounded wait)
             const uint64_t kDesc = sw128_desc(0, 16, 1024), sDesc = scale_desc(0);
             // stage s of the ring, its phase; the stage two back, its phase
             uint32_t s = 0, ph = 0, s2 = kStages - 2, ph2 = 1, it = 0, cS = tbase + kScales;
