@@ -220,6 +220,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 // returns when that one has ended and its writes are visible (at once where the launch was an ordinary one).
 // launch_dependents lets a kernel launched so behind this one start once every CTA has called it or ended; called
 // after grid_wait, the dependent sees the effects of everything before this kernel from its start.
+// What a kernel launched so reads may still be written while it is resident: grid_wait orders ordinary loads and bulk
+// copies behind it, but not loads of the read-only path (__ldg, ld.global.nc), which may only read what nothing writes
+// during the kernel's lifetime.  Such kernels use none.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

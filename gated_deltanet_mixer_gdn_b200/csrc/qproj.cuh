@@ -164,8 +164,8 @@ __device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t*
         const int u = tid + h * kRowThreads;
         a[h] = b[h] = make_uint4(0, 0, 0, 0);
         if (u < units) {
-            a[h] = __ldg(src + 2 * u);
-            b[h] = __ldg(src + 2 * u + 1);
+            a[h] = src[2 * u];
+            b[h] = src[2 * u + 1];
         }
     }
 #pragma unroll
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
         float* part = reinterpret_cast<float*>(smem);
         if constexpr (!kFuse) {
-            if (tid - 64 < p.T) s_gx[tid - 64] = split_scale(__ldg(p.gx + tid - 64));  // (T <= BN <= 128 threads)
+            if (tid - 64 < p.T) s_gx[tid - 64] = split_scale(p.gx[tid - 64]);  // (T <= BN <= 128 threads)
         }
         wait1(done, 0, kErrTimeoutMma);
         __syncwarp();
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         const int n = n0 + 4 * lane;
         float gw[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? __ldg(p.gw + n + e) : 0.0f;
+        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? p.gw[n + e] : 0.0f;
         int end;
         const GemmSegment g = segment_of(p, n, end);
         const bool whole = n + 4 <= end && (((n - g.col0) | g.ld) & 3) == 0;  // (segments start on 16 bytes)
@@ -727,8 +727,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             coords(t, tm, tn);
             const int row = tm * kTileM + 128 * rank + 32 * q4 + lane, n0 = tn * kTileN;
             float* gw = s_gw + (it & 1) * kTileN;
-            for (int i = et; i < kTileN; i += 256) gw[i] = n0 + i < p.N ? __ldg(p.gw + n0 + i) : 0.0f;
-            const float2 gx = split_scale(row < p.T ? __ldg(p.gx + row) : 1.0f);
+            for (int i = et; i < kTileN; i += 256) gw[i] = n0 + i < p.N ? p.gw[n0 + i] : 0.0f;
+            const float2 gx = split_scale(row < p.T ? p.gx[row] : 1.0f);
             named_barrier_sync(1, 256);
             wait1(&acc_full[it & 1], (it >> 1) & 1, kErrTimeoutMma);
             __syncwarp();

@@ -167,11 +167,12 @@ __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const qu
     const int w = tid >> 5, nw = step >> 5;                     // the row's warps
     uint4 next[4];
     auto load = [&](int g, int u, uint4(&x)[4]) {
-        const int row = g * blockDim.y + threadIdx.y;
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row * p.K) + 4 * u;
-        const bool in = row < p.rows && u < units;
+        // (past the row its last unit, past the last row that one: neither changes a maximum, and nothing is stored;
+        // cheaper than predicated loads of zeros: 16480 x 5120 nvfp4 39.7 us against 38.9)
+        const int row = min(static_cast<int>(g * blockDim.y + threadIdx.y), p.rows - 1);
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row * p.K) + 4 * min(u, units - 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = in ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) x[i] = src[i];
     };
     load(blockIdx.x, tid, next);
     for (int g = blockIdx.x, buf = 0; g < groups; g += gridDim.x, buf ^= 1) {
@@ -247,12 +248,12 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
     const int units = K / 16;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;  // (rows are multiples of 128 bytes)
     for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < rows; row += (int64_t)gridDim.x * blockDim.y) {
-        const float g = __ldg(row_scale + row);
+        const float g = row_scale[row];
         const uint2* src = reinterpret_cast<const uint2*>(codes + (size_t)row * (K / 2));
         uint4* dst = reinterpret_cast<uint4*>(out + (size_t)row * K);
         for (int u = threadIdx.x; u < units; u += blockDim.x) {
-            const uint2 c = __ldg(src + u);
-            const uint32_t sb = __ldg(scales + scale_offset(row, FMT == kNvfp4 ? u : u >> 1, tiles));
+            const uint2 c = src[u];
+            const uint32_t sb = scales[scale_offset(row, FMT == kNvfp4 ? u : u >> 1, tiles)];
             float s;
             if (FMT == kNvfp4) s = e4m3_value(sb);
             else s = sb == 255u ? __uint_as_float(0x7fc00000u) : (sb == 0u ? __uint_as_float(1u << 22) : __uint_as_float(sb << 23));
