@@ -1,6 +1,7 @@
 """Build libgdn_b200.so (sm_100a) in-tree with nvcc, and its debug variant
-libgdn_b200_debug.so (-DGDN_DEBUG: the kernels check the indices of their
-global-memory accesses and record a failed check in the device error word)."""
+libgdn_b200_debug.so (-DGDN_DEBUG: the kernels, but for the bf16 projections',
+check the indices of their global-memory accesses and record a failed check in
+the device error word)."""
 from __future__ import annotations
 
 import glob

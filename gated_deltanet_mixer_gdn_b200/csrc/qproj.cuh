@@ -91,6 +91,7 @@ __device__ __forceinline__ GemmSegment segment_of(const Params& p, int n, int& e
 __device__ __forceinline__ uint16_t* output_at(const Params& p, int n, int t) {
     int end;
     const GemmSegment g = segment_of(p, n, end);
+    if (!GDN_CHECK(t >= 0 && t < p.T && n >= g.col0 && n - g.col0 < g.ld)) return g.dst;
     return g.dst + (size_t)t * g.ld + (n - g.col0);
 }
 
@@ -163,7 +164,7 @@ __device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t*
     for (int h = 0; h < kHold; ++h) {
         const int u = tid + h * kRowThreads;
         a[h] = b[h] = make_uint4(0, 0, 0, 0);
-        if (u < units) {
+        if (u < units && GDN_CHECK(u >= 0 && row_of(u) < p.T)) {
             a[h] = src[2 * u];
             b[h] = src[2 * u + 1];
         }
@@ -275,19 +276,23 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
     if (warp == 0) {
         // ---------------- loads; a stage's bytes: codes of 128 features and BN tokens, their scale tiles
         auto scale_bytes = [&](int ks) { return min(kTiles, p.tiles - (k0 + ks) * kTiles) * quant::kTileBytes; };
+        // first byte of the stage's scale tiles in a row block
+        auto scale_at = [&](int ks) -> size_t {
+            const int tile = (k0 + ks) * kTiles;
+            return GDN_CHECK(tile >= 0 && tile < p.tiles && n0 < p.N) ? (size_t)tile * quant::kTileBytes : 0;
+        };
         auto load_w = [&](int ks, int s) {
             uint8_t* st = smem + s * C::STAGE_BYTES;
             mbar_arrive_expect_tx(&full[s], W_BYTES + (kFuse ? 0 : C::X_BYTES) + (kFuse ? 1 : 2) * scale_bytes(ks));
             tma_load_2d(st, &tmW, (k0 + ks) * (BK / 2), n0, &full[s]);
-            bulk_load(st + W_BYTES,
-                      p.sw + ((size_t)blockIdx.x * p.tiles + (k0 + ks) * kTiles) * quant::kTileBytes, scale_bytes(ks), &full[s]);
+            bulk_load(st + W_BYTES, p.sw + (size_t)blockIdx.x * p.tiles * quant::kTileBytes + scale_at(ks), scale_bytes(ks),
+                      &full[s]);
         };
         auto load_x = [&](int ks, int s) {
             if (kFuse) return;
             uint8_t* st = smem + s * C::STAGE_BYTES + W_BYTES + S_BYTES;
             tma_load_2d(st, &tmX, (k0 + ks) * (BK / 2), 0, &full[s]);
-            bulk_load(st + C::X_BYTES, p.sx + (size_t)(k0 + ks) * kTiles * quant::kTileBytes,
-                      scale_bytes(ks), &full[s]);
+            bulk_load(st + C::X_BYTES, p.sx + scale_at(ks), scale_bytes(ks), &full[s]);
         };
         const int head = min(C::kStages, ksteps);
         if (kFuse) grid_wait();
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int t = t0 + i * kWarps * split;
-                if (t < p.T) {
+                if (t < p.T && GDN_CHECK(t >= 0 && (n >= p.N || (n >= g.col0 && n - g.col0 < g.ld)))) {
                     const float2 gx = s_gx[t];
                     const uint32_t lo = scale_pack2(a[i].x, a[i].y, gx, gw[0], gw[1]);
                     const uint32_t hi = scale_pack2(a[i].z, a[i].w, gx, gw[2], gw[3]);
@@ -532,7 +537,7 @@ __device__ __forceinline__ void store_tile32x64(const Params& p, int t0, int c0,
         for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3);
             const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128_chunk(r, lane & 7));
-            if (t0 + r < p.T) *reinterpret_cast<uint4*>(dst + (size_t)r * g.ld) = v;
+            if (t0 + r < p.T && GDN_CHECK(t0 >= 0 && col >= 0 && col + 64 <= g.ld)) *reinterpret_cast<uint4*>(dst + (size_t)r * g.ld) = v;
         }
     } else if (t0 + lane < p.T) {  // segment boundaries, the last features, rows off 16 bytes
 #pragma unroll
@@ -543,6 +548,7 @@ __device__ __forceinline__ void store_tile32x64(const Params& p, int t0, int c0,
             const GemmSegment sg = segment_of(p, n, end);
             uint16_t* dst = sg.dst + (size_t)(t0 + lane) * sg.ld + (n - sg.col0);
             if (n + 8 <= end && (((n - sg.col0) | sg.ld) & 7) == 0) {
+                if (!GDN_CHECK(n >= sg.col0 && n + 8 - sg.col0 <= sg.ld)) continue;
                 *reinterpret_cast<uint4*>(dst) =
                     make_uint4(w[4 * (c & 3)], w[4 * (c & 3) + 1], w[4 * (c & 3) + 2], w[4 * (c & 3) + 3]);
             } else {

@@ -170,7 +170,9 @@ __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const qu
         // (past the row its last unit, past the last row that one: neither changes a maximum, and nothing is stored;
         // cheaper than predicated loads of zeros: 16480 x 5120 nvfp4 39.7 us against 38.9)
         const int row = min(static_cast<int>(g * blockDim.y + threadIdx.y), p.rows - 1);
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row * p.K) + 4 * min(u, units - 1);
+        const int uu = min(u, units - 1);
+        const bool ok = GDN_CHECK(row >= 0 && row < p.rows && uu >= 0 && (uu + 1) * kUnit <= p.K);
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (ok ? (size_t)row * p.K : 0)) + (ok ? 4 * uu : 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = src[i];
     };
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(quant::kMaxGroup) gdn_quantize_kernel(const qu
                 word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
             }
             constexpr int kLanes = FMT == kNvfp4 ? 2 : 4;
-            if (u < units) {
+            if (u < units && GDN_CHECK(u >= 0 && row < p.rows && (u + 1) * kUnit <= p.K && u / kLanes < p.tiles)) {
                 *reinterpret_cast<uint4*>(codes + 16 * u) = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 if ((lane & (kLanes - 1)) == 0)
                     *reinterpret_cast<uint32_t*>(scales + (u / kLanes) * kTileBytes) = word;
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(quant::kMaxGroup)
         const uint2* src = reinterpret_cast<const uint2*>(codes + (size_t)row * (K / 2));
         uint4* dst = reinterpret_cast<uint4*>(out + (size_t)row * K);
         for (int u = threadIdx.x; u < units; u += blockDim.x) {
+            if (!GDN_CHECK(row >= 0 && (u + 1) * 16 <= K && (FMT == kNvfp4 ? u : u >> 1) / 4 < tiles)) break;
             const uint2 c = src[u];
             const uint32_t sb = scales[scale_offset(row, FMT == kNvfp4 ? u : u >> 1, tiles)];
             float s;
