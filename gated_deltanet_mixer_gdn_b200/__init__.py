@@ -509,7 +509,7 @@ def _scale_shape(format: str, rows: int, K: int):
     return (rows + 127) // 128, -(-K // (4 * _QUANT_BLOCK[format])), 512
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)  # (compared and hashed by identity, as tensors are hashed)
 class QuantTensor:
     """Rows held in microscaled 4 bits (layouts in ``include/gdn.h``): what ``quantize`` returns and
     the 4-bit projections take as weights.  codes uint8 [rows, K/2]; scales uint8 [row blocks of 128,
