@@ -156,8 +156,8 @@ __device__ __forceinline__ void quantize_tokens(const qproj::Params& p, uint8_t*
     using namespace qproj;
     using namespace qproj::few;
     const int per_row = p.K / 16, units = p.T * per_row;  // units <= kRowThreads * kHold
-    const uint32_t inv = (0xffffffffu / per_row) + 1;                 // u / per_row by the high word, exact below 2^16
-    auto row_of = [&](int u) { return static_cast<int>(per_row == 1 ? u : __umulhi(static_cast<uint32_t>(u), inv)); };
+    const uint32_t inv = (0xffffffffu / per_row) + 1;  // u / per_row by the high word, exact below 2^16 (per_row >= 4)
+    auto row_of = [&](int u) { return static_cast<int>(__umulhi(static_cast<uint32_t>(u), inv)); };
     const uint4* src = reinterpret_cast<const uint4*>(p.x);
     uint4 a[kHold], b[kHold];
 #pragma unroll
