@@ -1439,9 +1439,11 @@ int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, i
     if (p.T <= 16) return qproj_few<FMT, 16, false>(cx, cw, p, nsm, stream);
     if (p.T <= 32) return qproj_few<FMT, 32, false>(cx, cw, p, nsm, stream);
     if (p.T <= 64) return qproj_few<FMT, 64, false>(cx, cw, p, nsm, stream);
-    // up to 128 tokens one pass over the weights by single CTAs, unless the pairs' tiles keep half of them busy
-    // (128 tokens: in_proj 21.1 us against 16.9 on 65 pairs, out_proj 12.4 against 14.9 on 20)
-    if (p.T <= 128 && (p.N + qproj::duo::kTileN - 1) / qproj::duo::kTileN < nsm / 4)
+    // Up to 96 tokens one pass over the weights by single CTAs; up to 128 too, unless the pairs' tiles keep two thirds
+    // of them busy.  us by single CTAs / by pairs, nvfp4, at 65, 96 and 128 tokens: 16480 x 5120 (65 pair tiles)
+    // 15.5 / 16.8, 16.4 / 16.9, 17.9 / 17.4; 12352 x 5120 (49) 15.2 / 15.9, 15.9 / 15.9, 17.2 / 16.4; 10240 x 6144 (40)
+    // 14.9 / 16.4, 15.5 / 16.5, 16.5 / 17.1; 12288 x 6144 (48) 15.4 / 17.0, 15.9 / 17.0, 16.9 / 17.6; 5120 x 6144 (20) 10.3 / 14.4, 11.3 / 14.9, 12.1 / 15.2.
+    if (p.T <= 96 || (p.T <= 128 && (p.N + qproj::duo::kTileN - 1) / qproj::duo::kTileN < nsm / 3))
         return qproj_few<FMT, 128, false>(cx, cw, p, nsm, stream);
     return qproj_pairs<FMT>(cx, cw, p, nsm, stream);
 }
