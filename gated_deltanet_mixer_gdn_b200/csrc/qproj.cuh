@@ -272,27 +272,27 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
             record_error(code);
         }
     };
+    const int n = n0 + 4 * lane;  // a lane's four features of the output, and their row scales
+    float gw[4];
 
     if (warp == 0) {
         // ---------------- loads; a stage's bytes: codes of 128 features and BN tokens, their scale tiles
         auto scale_bytes = [&](int ks) { return min(kTiles, p.tiles - (k0 + ks) * kTiles) * quant::kTileBytes; };
-        // first byte of the stage's scale tiles in a row block
-        auto scale_at = [&](int ks) -> size_t {
-            const int tile = (k0 + ks) * kTiles;
-            return GDN_CHECK(tile >= 0 && tile < p.tiles && n0 < p.N) ? (size_t)tile * quant::kTileBytes : 0;
-        };
+        auto tile_ok = [&](int ks) { return GDN_CHECK(k0 + ks >= 0 && (k0 + ks) * kTiles < p.tiles && n0 < p.N); };
         auto load_w = [&](int ks, int s) {
             uint8_t* st = smem + s * C::STAGE_BYTES;
             mbar_arrive_expect_tx(&full[s], W_BYTES + (kFuse ? 0 : C::X_BYTES) + (kFuse ? 1 : 2) * scale_bytes(ks));
             tma_load_2d(st, &tmW, (k0 + ks) * (BK / 2), n0, &full[s]);
-            bulk_load(st + W_BYTES, p.sw + (size_t)blockIdx.x * p.tiles * quant::kTileBytes + scale_at(ks), scale_bytes(ks),
-                      &full[s]);
+            bulk_load(st + W_BYTES,
+                      p.sw + (tile_ok(ks) ? ((size_t)blockIdx.x * p.tiles + (k0 + ks) * kTiles) * quant::kTileBytes : 0),
+                      scale_bytes(ks), &full[s]);
         };
         auto load_x = [&](int ks, int s) {
             if (kFuse) return;
             uint8_t* st = smem + s * C::STAGE_BYTES + W_BYTES + S_BYTES;
             tma_load_2d(st, &tmX, (k0 + ks) * (BK / 2), 0, &full[s]);
-            bulk_load(st + C::X_BYTES, p.sx + scale_at(ks), scale_bytes(ks), &full[s]);
+            bulk_load(st + C::X_BYTES, p.sx + (tile_ok(ks) ? (size_t)(k0 + ks) * kTiles * quant::kTileBytes : 0),
+                      scale_bytes(ks), &full[s]);
         };
         const int head = min(C::kStages, ksteps);
         if (kFuse) grid_wait();
@@ -357,6 +357,8 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         }
     } else {
         grid_wait();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? p.gw[n + e] : 0.0f;  // (used behind the sums: loaded ahead of them)
         if constexpr (kFuse) quantize_tokens<FMT, C>(p, smem + C::OFF_X, s_amax, s_gx, rows_ready, tid - 64, k0, ksteps);
         // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
@@ -383,10 +385,6 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
     if (warp >= 2) {
         // ---------------- this rank's tokens: four features per lane, a token's 128 per warp
         constexpr int kWarps = C::kThreads / 32 - 2, kBatch = 4;  // a warp's tokens, kBatch of them at once
-        const int n = n0 + 4 * lane;
-        float gw[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? p.gw[n + e] : 0.0f;
         int end;
         const GemmSegment g = segment_of(p, n, end);
         const bool whole = n + 4 <= end && (((n - g.col0) | g.ld) & 3) == 0;  // (segments start on 16 bytes)
