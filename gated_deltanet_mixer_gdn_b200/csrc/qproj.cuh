@@ -357,9 +357,11 @@ __global__ void __launch_bounds__(qproj::few::Cfg<BN, kFuse>::kThreads, 1)
         }
     } else {
         grid_wait();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? p.gw[n + e] : 0.0f;  // (used behind the sums: loaded ahead of them)
         if constexpr (kFuse) quantize_tokens<FMT, C>(p, smem + C::OFF_X, s_amax, s_gx, rows_ready, tid - 64, k0, ksteps);
+        // (the features' row scales, used behind the sums, are loaded ahead of them, but not ahead of the tokens: 3 tokens
+        // 12.4 us, 13.2 so)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gw[e] = n + e < p.N ? p.gw[n + e] : 0.0f;
         // ---------------- sums -> shared memory [token][feature] (the ring: every product has read it)
         const int q4 = warp & 3;  // TMEM lane quarter of this warp
         float* part = reinterpret_cast<float*>(smem);
@@ -754,8 +756,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(qproj::duo::kDuoThre
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            // relaxed: the columns are in registers (tmem_ld_wait), there is nothing else to publish; a release
-            // at cluster scope would wait for the previous tile's output stores (about 1,300 cycles a tile)
+            // Relaxed: the order that the next products need does not come from the arrival's own semantics.  Tensor
+            // memory is ordered by the tcgen05 operations: wait::ld completes the loads, fence::before_thread_sync
+            // orders them before whatever instruction signals the other thread, and the issuer's
+            // fence::after_thread_sync behind its wait orders its products after that.  Nothing else is handed over
+            // (the row scales in s_gw are this CTA's epilogue's own); a release at cluster scope would wait for the
+            // previous tile's output stores, about 1,300 cycles a tile.
             if (lane == 0)
                 asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(free_bar) : "memory");
             uint8_t* stage = smem + OFF_OUT + (warp - 2) * kOutBytes;
