@@ -1448,10 +1448,14 @@ int qproj_launch(const uint8_t* cx, const uint8_t* cw, const qproj::Params& p, i
     return qproj_pairs<FMT>(cx, cw, p, nsm, stream);
 }
 
-// Whether a projection quantises its few tokens itself: at most 16384 elements, which fit its threads'
-// registers, of rows that fit its shared memory.  In_proj of 5120 -> 16480, nvfp4, as a graph: 1 token 13.3 -> 11.9
-// us, 2 tokens 13.0 -> 12.3; every CTA repeating the quantisation of more costs more than the launch it saves (4
-// tokens 12.9 -> 14.2, 8 tokens 13.4 -> 16.3).
+// Whether a projection quantises its few tokens itself: at most 16 tokens and 16384 elements, which fit its threads'
+// registers, of rows that fit its shared memory.  The rule is in T and K alone because the workspace's size, which the
+// caller asks for by T and K, follows from it: such calls need none.  Every CTA repeats the quantisation, so it pays
+// where its weights' loads cover it.  us so / by a launch of its own, nvfp4: 16480 x 5120, 1 token 11.3 / 12.3, 2 tokens
+// 11.3 / 12.5, 3 tokens 12.3 / 12.4; 16480 x 1024, 1 token 5.1 / 5.6, 4 tokens 5.2 / 5.7, 8 tokens 5.7 / 5.2, 16 tokens
+// 6.2 / 5.7; 5120 x 6144 (K shared by 3 CTAs, each scanning whole rows), 1 token 7.7 / 7.7, 2 tokens 8.2 / 7.7;
+// 4120 x 1088, 1 token 5.7 / 5.7, 15 tokens 7.2 / 5.7.  More elements would lose everywhere (before it had this bound:
+// 16480 x 5120, 8 tokens 16.3 against 13.4).
 bool few_fuse(int64_t T, int K) {
     return T <= 16 && T * (K / 16) <= qproj::few::kRowThreads * qproj::few::kHold &&
            K <= qproj::few::kMaxSteps * qproj::BK;

@@ -130,7 +130,7 @@ struct Cfg {
     static constexpr uint32_t X_BYTES = BN * BK / 2;
     static constexpr uint32_t X_STAGE = X_BYTES + S_BYTES;  // a stage's token codes and scales
     static constexpr uint32_t STAGE_BYTES = W_BYTES + S_BYTES + (kFuse ? 0 : X_STAGE);
-    static constexpr int kStages = kFuse ? 7 : 6;  // (more: 64 tokens 16.5 us with 7 against 16.1, 32 tokens 14.5 with 9 against 13.9)
+    static constexpr int kStages = kFuse ? 7 : 6;  // (more: 64 tokens 14.5 us with 7 against 14.4, 32 tokens 13.6 with 9 against 13.2)
     static constexpr uint32_t OFF_X = kStages * STAGE_BYTES;  // (kFuse) all stages' tokens
     static constexpr uint32_t OFF_MISC = OFF_X + (kFuse ? kMaxSteps * X_STAGE : 0);
     static constexpr uint32_t OFF_AMAX = OFF_MISC + 256 + BN * 8;  // (kFuse) behind the row scales

@@ -335,8 +335,8 @@ int gdn_dequantize(int32_t format, int32_t rows, int32_t K, const uint8_t* codes
  * leave f32's range only where the result does) and rounded once to bf16.
  * Outputs as for gdn_in_proj / gdn_out_proj, 16-byte aligned.
  * workspace: gdn_proj_quant_workspace_size(format, T, K) bytes (the quantised
- * tokens; 0 for a few tokens, which the projection quantises on chip: NULL is
- * legal then), 16-byte aligned.  K a multiple of 64 (GDN_ERR_UNSUPPORTED
+ * tokens; 0 for a few tokens, T <= 16, T * K <= 16384 and K <= 6144, which the
+ * projection quantises on chip: NULL is legal then), 16-byte aligned.  K a multiple of 64 (GDN_ERR_UNSUPPORTED
  * otherwise).  T = 0 is a legal no-op.  Asynchronous on `stream`.
  */
 size_t gdn_proj_quant_workspace_size(int32_t format, int32_t T, int32_t K);
